@@ -297,6 +297,55 @@ zipnn_status zipnn_shard_tables(zipnn_dtype dtype, uint32_t chunk_bytes, uint32_
                                 const uint64_t* all_sizes, uint32_t rank, uint32_t world, void* ws, size_t ws_bytes,
                                 zipnn_stream_t stream);
 
+/* ---- Microscaled 4-bit tensors --------------------------------------------------------
+ * The FP4 (E2M1) tensors that the codec stores, as a program makes and uses them: a matrix
+ * of rows x cols values, each row cut into blocks of values that share one scale.
+ *   ZIPNN_MXFP4: blocks of 32, scales E8M0 (byte b stands for 2^(b - 127), 255 for NaN).
+ *   ZIPNN_NVFP4: blocks of 16, scales E4M3 (not negative), and one FP32 scale of the tensor.
+ * A value is (its E2M1 code) x (its block's scale) x (the tensor's scale, NVFP4).
+ * Codes: rows of zipnn_mx_row_bytes(cols) bytes, two codes to a byte, the first in the low
+ * nibble (as ZIPNN_FP4_E2M1; the codec takes them with n = 2 * rows * row bytes). The row's
+ * last bytes are padded with zero codes to whole 32 values.
+ * Scales: tiles of 128 rows x 4 blocks, 512 bytes each, tile (row / 128, block / 4) at
+ * 512 * (row / 128 * ceil(blocks / 4) + block / 4), row-and-block at
+ * 16 * (row % 32) + 4 * (row / 32 % 4) + block % 4 in it: the order in which the tensor cores
+ * take them. Bytes of rows and blocks past the matrix are zero; every call reads them so.
+ * Device pointers are 16-byte aligned except where a call says otherwise. */
+typedef enum { ZIPNN_MXFP4 = 0, ZIPNN_NVFP4 = 1 } zipnn_mx_format;
+/* Types of plain values (not those of zipnn_dtype: FP16 is not a type of the codec). */
+typedef enum { ZIPNN_VALUE_BF16 = 0, ZIPNN_VALUE_FP32 = 1, ZIPNN_VALUE_FP16 = 2 } zipnn_value_type;
+
+/* Bytes of one row of codes: 16 * ceil(cols / 32). */
+size_t zipnn_mx_row_bytes(uint64_t cols);
+/* Bytes of the scale tiles; 0 for invalid arguments. */
+size_t zipnn_mx_scale_bytes(zipnn_mx_format format, uint64_t rows, uint64_t cols);
+/* Workspace bytes of zipnn_mx_quantize with find_global (16-byte aligned, no contents kept). */
+#define ZIPNN_MX_WORKSPACE_BYTES 4096u
+
+/* Quantise the matrix at `x` (device, aligned to its values; row r at x + r * row_stride
+ * values, row_stride >= cols) into `codes` and `scales` (device).
+ *   MXFP4: scale 2^(floor(log2(amax)) - 2), the exponent kept in [-127, 127], amax = the
+ *   block's largest magnitude; code = x / scale to the nearest E2M1 value, ties to the even
+ *   code, at most 6. global_scale and ws are not used and may be NULL.
+ *   NVFP4: with g = *global_scale (device; positive and finite), scale s = amax / (6 g) to the
+ *   nearest E4M3 value (ties to even), at most 448; code = x / (s g), rounded likewise, and a
+ *   zero of x's sign where s is 0. With find_global, g is first computed from the matrix and
+ *   stored at *global_scale: the FP32 quotient of its largest finite magnitude by 2688
+ *   (= 448 * 6), or 1 where that is 0; this reads x twice.
+ * Every quotient is rounded once, as if computed exactly: no result depends on how the work
+ * is split. A block that holds an infinity or a NaN gets a NaN scale (255, or 127 for E4M3)
+ * and zero codes. Asynchronous, allocates nothing. */
+zipnn_status zipnn_mx_quantize(zipnn_mx_format format, zipnn_value_type type, const void* x, uint64_t rows,
+                               uint64_t cols, uint64_t row_stride, float* global_scale, int find_global, void* codes,
+                               void* scales, void* ws, size_t ws_bytes, zipnn_stream_t stream);
+
+/* The values of a microscaled matrix, to `out` (device, aligned to its values; row r at
+ * out + r * row_stride values): code x scale in FP32 (exact but for overflow), times
+ * *global_scale for NVFP4 (rounded to FP32), then rounded to `type`. Asynchronous. */
+zipnn_status zipnn_mx_dequantize(zipnn_mx_format format, zipnn_value_type type, const void* codes, const void* scales,
+                                 const float* global_scale, uint64_t rows, uint64_t cols, void* out,
+                                 uint64_t row_stride, zipnn_stream_t stream);
+
 /* Compress without allocating (the pages have no counterpart of this call). For callers
  * that cannot allocate device memory: code whose device memory is owned by a framework's
  * caching allocator that it cannot reach from C (a cudaMalloc of its own would fight

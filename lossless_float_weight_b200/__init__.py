@@ -8,7 +8,7 @@ machine where the library has not been built.
 """
 import importlib
 
-_SUBMODULES = ("workloads", "zipnn", "build")
+_SUBMODULES = ("workloads", "zipnn", "build", "mx", "pages")
 
 
 def __getattr__(name):

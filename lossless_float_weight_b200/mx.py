@@ -1,0 +1,214 @@
+"""Microscaled 4-bit tensors: made, read back, and stored compressed.
+
+A matrix of E2M1 values whose blocks share a scale ("mxfp4": 32 values, E8M0 scales;
+"nvfp4": 16 values, E4M3 scales and one FP32 scale of the tensor), in the layout of
+include/zipnn.h. The codes are what the codec stores as FP4 and the scales as FP8, so a
+quantised weight or K/V cache goes through :func:`compress` and comes back bit for bit::
+
+    q = mx.quantize(w)                  # w: (..., K) BF16, FP16 or FP32
+    w4 = mx.dequantize(q)               # BF16 values
+    c = mx.compress(q)                  # two containers of the codec
+    q2 = mx.decompress(c)               # the same codes and scales
+
+The functions check their arguments, allocate with PyTorch and call the CUDA library on
+the current stream of the tensors' device (or `stream`); they do not synchronise, except
+:func:`compress` and :func:`decompress`, as the codec's own.
+"""
+import torch
+
+from . import zipnn as Z
+
+BLOCK = {"mxfp4": 32, "nvfp4": 16}
+_FORMATS = {"mxfp4": Z.MXFP4, "nvfp4": Z.NVFP4}
+_SCALE_DTYPES = {"mxfp4": torch.float8_e8m0fnu, "nvfp4": torch.float8_e4m3fn}
+_VALUES = {torch.bfloat16: Z.VALUE_BF16, torch.float32: Z.VALUE_FP32, torch.float16: Z.VALUE_FP16}
+
+
+def _fail(what):
+    raise Z.ZipnnError(Z.ERR_INVALID_ARG, what)
+
+
+def _format(format):
+    f = _FORMATS.get(format)
+    return f if f is not None else _fail(f"mx: format {format!r} is not one of {sorted(_FORMATS)}")
+
+
+def _call(fn, what, device, *args):
+    """fn(*args, stream) on the current stream of the tensors' device, made current."""
+    if device.index == torch.cuda.current_device():
+        Z.check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+    else:
+        with torch.cuda.device(device):
+            Z.check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+
+
+def _use(stream, device):
+    """`stream` (a torch stream or a raw handle on `device`) as the current one: what a call
+    allocates then belongs to the stream that writes it."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+
+
+def _rows(shape):
+    n = 1
+    for d in shape[:-1]:
+        n *= d
+    return n
+
+
+class MxTensor:
+    """A microscaled 4-bit tensor of `shape` (its last dimension in blocks).
+
+    codes: one row of zipnn_mx_row_bytes(shape[-1]) bytes for each row of the flattened
+    leading dimensions (torch.float4_e2m1fn_x2 or uint8, contiguous); scales: the 1-D tiles
+    of the blocks' scales (one byte each); global_scale: a one-element FP32 CUDA tensor for
+    "nvfp4", None for "mxfp4". A tensor without rows has empty codes and scales."""
+
+    __slots__ = ("codes", "scales", "shape", "format", "global_scale", "rows", "cols")
+
+    def __init__(self, codes, scales, shape, format, global_scale=None):
+        f = _format(format)
+        self.codes, self.scales, self.format, self.global_scale = codes, scales, format, global_scale
+        self.shape = shape if type(shape) is tuple else tuple(shape)
+        if not self.shape or min(self.shape) < 0 or self.shape[-1] == 0:
+            _fail("MxTensor: at least one dimension, the last not empty")
+        self.cols = self.shape[-1]
+        self.rows = self.shape[0] if len(self.shape) == 2 else _rows(self.shape)
+        if not (codes.is_cuda and codes.is_contiguous() and codes.element_size() == 1 and
+                codes.numel() == self.rows * Z.zipnn_mx_row_bytes(self.cols)):
+            _fail("MxTensor: codes are rows x zipnn_mx_row_bytes(cols) contiguous CUDA bytes")
+        if not (scales.device == codes.device and scales.is_contiguous() and scales.element_size() == 1 and
+                scales.numel() == (Z.zipnn_mx_scale_bytes(f, self.rows, self.cols) if self.rows else 0)):
+            _fail("MxTensor: scales are zipnn_mx_scale_bytes contiguous bytes beside the codes")
+        if f == Z.NVFP4:
+            g = global_scale
+            if g is None or g.dtype != torch.float32 or g.numel() != 1 or g.device != codes.device:
+                _fail("MxTensor: nvfp4 has a global_scale, one FP32 value on the codes' device")
+        elif global_scale is not None:
+            _fail("MxTensor: mxfp4 has no global_scale")
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def _global(self):
+        return None if self.global_scale is None else self.global_scale.data_ptr()
+
+    def block_scales(self):
+        """The scales as a (rows, blocks) tensor, one to a block (a copy)."""
+        nb = -(-self.cols // BLOCK[self.format])
+        t = self.scales.view(torch.uint8).view(-(-self.rows // 128), -(-nb // 4), 32, 4, 4)
+        return t.permute(0, 3, 2, 1, 4).reshape(-1, 4 * t.shape[1])[:self.rows, :nb].contiguous().view(self.scales.dtype)
+
+
+def tile_scales(block_scales):
+    """A (rows, blocks) tensor of one-byte scales in the tiles of MxTensor.scales."""
+    r, nb = block_scales.shape
+    s = torch.nn.functional.pad(block_scales.view(torch.uint8), (0, -nb % 4, 0, -r % 128))
+    s = s.view(-(-r // 128), 4, 32, -(-nb // 4), 4).permute(0, 3, 2, 1, 4)
+    return s.reshape(-1).view(block_scales.dtype)
+
+
+def quantize(x, format="mxfp4", global_scale=None, stream=None):
+    """Quantise the CUDA tensor x (..., K) in blocks along its last dimension.
+
+    nvfp4: global_scale is a one-element FP32 CUDA tensor (positive; taken as it is), or None:
+    then it is found from x (its largest finite magnitude / 2688). Rounding, saturation and
+    what a block with a NaN gives: zipnn_mx_quantize."""
+    if stream is not None:
+        with _use(stream, x.device):
+            return quantize(x, format, global_scale)
+    f = _format(format)
+    if x.dtype not in _VALUES or not x.is_cuda or x.dim() == 0 or x.shape[-1] == 0:
+        _fail("mx.quantize: a CUDA tensor (..., K) of BF16, FP16 or FP32")
+    shape, dev = tuple(x.shape), x.device
+    cols = shape[-1]
+    m = x if x.dim() == 2 else x.reshape(-1, cols)
+    rows = m.shape[0]
+    if (cols > 1 and m.stride(1) != 1) or (rows > 1 and m.stride(0) < cols):
+        m = m.contiguous()
+    if f == Z.NVFP4:
+        find = global_scale is None
+        if find:
+            global_scale = torch.empty(1, dtype=torch.float32, device=dev)
+        elif global_scale.dtype != torch.float32 or global_scale.numel() != 1 or global_scale.device != dev:
+            _fail("mx.quantize: global_scale is one FP32 value on x's device")
+    else:
+        find = False
+        if global_scale is not None:
+            _fail("mx.quantize: mxfp4 has no global_scale")
+    if rows == 0:
+        if find:
+            global_scale.fill_(1.0)
+        return MxTensor(torch.empty((0,), dtype=torch.uint8, device=dev),
+                        torch.empty((0,), dtype=_SCALE_DTYPES[format], device=dev), shape, format, global_scale)
+    rb, sb = Z.zipnn_mx_row_bytes(cols), Z.zipnn_mx_scale_bytes(f, rows, cols)
+    if sb == 0:
+        _fail("mx.quantize: at most 2^31 rows and columns")
+    codes = torch.empty((rows, rb), dtype=torch.float4_e2m1fn_x2, device=dev)
+    scales = torch.empty((sb,), dtype=_SCALE_DTYPES[format], device=dev)
+    ws = torch.empty((Z.MX_WORKSPACE_BYTES,), dtype=torch.uint8, device=dev) if find else None
+    _call(Z.zipnn_mx_quantize, "zipnn_mx_quantize", dev, f, _VALUES[x.dtype], m.data_ptr(), rows, cols,
+          m.stride(0) if rows > 1 else cols, None if global_scale is None else global_scale.data_ptr(), int(find),
+          codes.data_ptr(), scales.data_ptr(), ws.data_ptr() if find else None, Z.MX_WORKSPACE_BYTES if find else 0)
+    return MxTensor(codes, scales, shape, format, global_scale)
+
+
+def _out(out, shape, dtype, device, what):
+    """A new tensor, or the caller's where it can be written: its last dimension contiguous."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
+        _fail(f"{what}: out is a {dtype} tensor {tuple(shape)} on {device}")
+    if not (out.is_contiguous() or (out.dim() == 2 and (out.shape[1] == 1 or out.stride(1) == 1) and out.stride(0) >= out.shape[1])):
+        _fail(f"{what}: out's rows are contiguous and do not overlap")
+    return out
+
+
+def dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of q as a tensor of its shape (BF16, FP16 or FP32)."""
+    if stream is not None:
+        with _use(stream, q.device):
+            return dequantize(q, dtype, out)
+    if dtype not in _VALUES:
+        _fail("mx.dequantize: to BF16, FP16 or FP32")
+    out = _out(out, q.shape, dtype, q.device, "mx.dequantize")
+    if q.rows:
+        stride = out.stride(0) if out.dim() == 2 and q.rows > 1 else q.cols
+        _call(Z.zipnn_mx_dequantize, "zipnn_mx_dequantize", q.device, _FORMATS[q.format], _VALUES[dtype],
+              q.codes.data_ptr(), q.scales.data_ptr(), q._global, q.rows, q.cols, out.data_ptr(), stride)
+    return out
+
+
+class MxContainers:
+    """A microscaled tensor compressed: a container of its codes (FP4) and one of its scales
+    (as FP8 values), and what it takes to put them together again."""
+
+    def __init__(self, codes, scales, shape, format, global_scale, chunk_bytes):
+        self.codes, self.scales, self.shape, self.format = codes, scales, shape, format
+        self.global_scale, self.chunk_bytes = global_scale, chunk_bytes
+
+    @property
+    def nbytes(self):
+        return self.codes.numel() + self.scales.numel()
+
+
+def compress(q, chunk_bytes=Z.DEFAULT_CHUNK_BYTES, plan=None, stream=None):
+    """Compress a microscaled tensor's codes (with `plan`, an FP4 plan, if given) and scales
+    with the codec (synchronises)."""
+    if q.rows == 0:
+        _fail("mx.compress: an empty tensor")
+    with torch.cuda.device(q.device):
+        codes = Z.compress(q.codes.view(torch.float4_e2m1fn_x2), chunk_bytes, plan, stream=stream)
+        scales = Z.compress(q.scales.view(torch.float8_e4m3fn), chunk_bytes, stream=stream)
+    return MxContainers(codes, scales, q.shape, q.format, q.global_scale, chunk_bytes)
+
+
+def decompress(c, stream=None):
+    """The microscaled tensor of mx.compress, bit for bit (synchronises)."""
+    rows, cols = _rows(c.shape), c.shape[-1]
+    with torch.cuda.device(c.codes.device):
+        codes = Z.decompress(c.codes, torch.float4_e2m1fn_x2, (rows, Z.zipnn_mx_row_bytes(cols)), c.chunk_bytes, stream)
+        scales = Z.decompress(c.scales, torch.float8_e4m3fn, (Z.zipnn_mx_scale_bytes(_FORMATS[c.format], rows, cols),),
+                              c.chunk_bytes, stream)
+    return MxTensor(codes, scales.view(_SCALE_DTYPES[c.format]), c.shape, c.format, c.global_scale)

@@ -82,6 +82,15 @@ zipnn_shard_sizes = _sig("zipnn_shard_sizes", _i, _u32, ctypes.POINTER(ShardItem
 zipnn_shard_tables = _sig("zipnn_shard_tables", _i, _i, _u32, _u32, ctypes.POINTER(ShardItem), _vp, _u32, _u32, _vp,
                           _sz, _vp)
 
+MXFP4, NVFP4 = 0, 1
+VALUE_BF16, VALUE_FP32, VALUE_FP16 = 0, 1, 2
+MX_WORKSPACE_BYTES = 4096
+
+zipnn_mx_row_bytes = _sig("zipnn_mx_row_bytes", _sz, _u64)
+zipnn_mx_scale_bytes = _sig("zipnn_mx_scale_bytes", _sz, _i, _u64, _u64)
+zipnn_mx_quantize = _sig("zipnn_mx_quantize", _i, _i, _i, _vp, _u64, _u64, _u64, _vp, _i, _vp, _vp, _vp, _sz, _vp)
+zipnn_mx_dequantize = _sig("zipnn_mx_dequantize", _i, _i, _i, _vp, _vp, _vp, _u64, _u64, _vp, _u64, _vp)
+
 C_ABI_NAMES = [
     "zipnn_max_compressed_bytes", "zipnn_workspace_bytes", "zipnn_compress", "zipnn_compress_ex",
     "zipnn_decompress", "zipnn_compressed_size", "zipnn_get_status", "zipnn_histogram", "zipnn_code_lengths",
@@ -89,7 +98,7 @@ C_ABI_NAMES = [
     "zipnn_status_string", "zipnn_timing_enable", "zipnn_timing_collect", "zipnn_kernel_count",
     "zipnn_kernel_name", "zipnn_compress_noalloc", "zipnn_decompress_batch_workspace_bytes",
     "zipnn_decompress_batch", "zipnn_test_lookback_limit", "zipnn_shard_workspace_bytes", "zipnn_shard_sizes",
-    "zipnn_shard_tables",
+    "zipnn_shard_tables", "zipnn_mx_row_bytes", "zipnn_mx_scale_bytes", "zipnn_mx_quantize", "zipnn_mx_dequantize",
 ]
 
 
