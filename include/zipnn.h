@@ -346,6 +346,78 @@ zipnn_status zipnn_mx_dequantize(zipnn_mx_format format, zipnn_value_type type, 
                                  const float* global_scale, uint64_t rows, uint64_t cols, void* out,
                                  uint64_t row_stride, zipnn_stream_t stream);
 
+/* ---- Pages of a K/V cache ------------------------------------------------------------
+ * A served K/V cache lies in pages: page p of a pool holds `page_tokens` positions of one
+ * sequence, in each of `planes` arrays (K and V of each layer). Sequences that start alike
+ * share pages. These calls move pages (between places of a pool, and to and from the
+ * contiguous tensors that the codec takes) and keep the sequences' books:
+ *   refs[p]             how many sequences hold page p; 0 for a free page
+ *   lens[row]           positions of the sequence in `row`; 0 for an empty row
+ *   tables[row][slot]   the page of positions slot * page_tokens and on, for slots below
+ *                       ceil(lens[row] / page_tokens); -1 past them
+ * Only whole pages are shared, so a sequence may write behind its last position without
+ * asking. All are device memory of the caller's, changed in place and in stream order.
+ * Everything is asynchronous, allocates nothing and is deterministic. Errors found on the
+ * device go to the workspace's status (the first stays until the caller clears the
+ * workspace), where zipnn_get_status reads it: the caller zeroes a new workspace once. One
+ * workspace must not be used by two calls that may run at the same time. */
+typedef struct zipnn_page_pool {
+  void* base;            /* device, 16-byte aligned: page 0 of plane 0 */
+  uint64_t plane_stride; /* bytes, multiples of 16; pages do not overlap */
+  uint64_t page_stride;
+  uint32_t planes, pages;
+} zipnn_page_pool;
+
+typedef struct zipnn_page_table {
+  int32_t* refs;   /* pages */
+  int32_t* lens;   /* seqs */
+  int32_t* tables; /* seqs x slots */
+  uint32_t seqs, slots, page_tokens; /* seqs at most 2^18, seqs x slots below 2^31 */
+} zipnn_page_table;
+
+/* Workspace bytes (device, 16-byte aligned) of zipnn_pages_fork and zipnn_pages_free;
+ * zipnn_pages_copy needs 256. */
+size_t zipnn_pages_workspace_bytes(uint32_t seqs, uint32_t pages);
+
+/* Copy `count` pages of page_bytes (a multiple of 16) in every plane: pair i from page
+ * src_ids[i] of src to page dst_ids[i] of dst (device lists; NULL: page i; a negative number
+ * skips the pair). src and dst are the same pool, or do not overlap. Refused with
+ * ZIPNN_ERR_INVALID_ARG in the status, and then nothing copied: a destination named twice,
+ * and within one pool a destination that is also a source. A number past the pool's pages
+ * gives the same status; with dst_ids NULL the other pairs are then copied all the same. */
+zipnn_status zipnn_pages_copy(const zipnn_page_pool* src, const int32_t* src_ids, const zipnn_page_pool* dst,
+                              const int32_t* dst_ids, uint32_t count, uint64_t page_bytes, void* ws, size_t ws_bytes,
+                              zipnn_stream_t stream);
+
+/* `count` sequences get their pages (device lists of row, parent and length): the row j
+ * becomes lens[j] positions long.
+ *   parent -1: a new sequence, of fresh pages;
+ *   parent another row: it starts as the parent does: whole pages below min(its length, the
+ *   parent's) are shared, the page in which that ends is copied to a fresh one, and fresh
+ *   pages follow to its length;
+ *   parent = the row itself: it grows (or stays), by fresh pages behind those it has.
+ * A row that does not grow has to be empty. Fresh pages are the lowest free ones, in the
+ * order of the requests; their contents are left as they were. Parents are read as they
+ * were before the call. All or nothing: numbers out of range, a row named twice, a row not
+ * empty, a length below a growing row's or past the table set ZIPNN_ERR_INVALID_ARG, too few
+ * free pages ZIPNN_ERR_OUT_TOO_SMALL, and nothing is changed. A parent's table that names
+ * pages outside the pool sets ZIPNN_ERR_CORRUPT. */
+zipnn_status zipnn_pages_fork(const zipnn_page_pool* pool, uint64_t page_bytes, const zipnn_page_table* table,
+                              const int32_t* rows, const int32_t* parents, const int32_t* lens, uint32_t count, void* ws,
+                              size_t ws_bytes, zipnn_stream_t stream);
+
+/* The sequences in `count` rows (device list; a row named twice is freed once, an empty one
+ * is left empty) give their pages back: references fall by one each, and the rows are
+ * cleared. A row out of range sets ZIPNN_ERR_INVALID_ARG and is passed over; a table that
+ * does not fit the references sets ZIPNN_ERR_CORRUPT.
+ * With `compact`, the gaps are then closed: of `live` pages in use, those numbered live and
+ * up move, in order, into the free numbers below live, in order: their contents, their
+ * references, and their numbers in every table. The u32 at ws + 4 receives `live`. With
+ * count 0 this is the closing alone. */
+zipnn_status zipnn_pages_free(const zipnn_page_pool* pool, uint64_t page_bytes, const zipnn_page_table* table,
+                              const int32_t* rows, uint32_t count, int compact, void* ws, size_t ws_bytes,
+                              zipnn_stream_t stream);
+
 /* Compress without allocating (the pages have no counterpart of this call). For callers
  * that cannot allocate device memory: code whose device memory is owned by a framework's
  * caching allocator that it cannot reach from C (a cudaMalloc of its own would fight

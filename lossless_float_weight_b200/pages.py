@@ -1,0 +1,214 @@
+"""Pages of a served K/V cache: copied, shared when a sequence forks, given back, closed up,
+and stored compressed.
+
+A pool is one CUDA tensor of shape (planes, pages, ...): page p of a plane holds
+`page_tokens` positions of the K or V of one layer. :class:`PagePool` keeps beside it which
+sequence holds which page (the references, lengths and tables of include/zipnn.h)::
+
+    pool = pages.PagePool(kv, page_tokens=16, max_seqs=64, max_pages=256)
+    pool.fork([0], [-1], [700])          # sequence 0: 700 positions, fresh pages
+    pool.fork([1], [0], [650])           # sequence 1: its first 650, shared where whole
+    stored = pool.store(0)               # sequence 0's pages through the codec
+    pool.free([0], compact=True)         # its references back, and the gaps closed
+    pool.load(stored, 2)                 # the same positions in row 2
+
+`fork`, `free`, `compact`, `copy` and `gather` only launch kernels on the current stream (or
+`stream`); what they find wrong is read with `status()`. `store` and `load` synchronise.
+"""
+import ctypes
+
+import torch
+
+from . import zipnn as Z
+from .mx import _call, _fail, _use
+
+# types of the codec, and the ones it stores by their bits
+_CODEC = {torch.float16: torch.bfloat16, torch.uint8: torch.float8_e4m3fn, torch.int8: torch.float8_e4m3fn,
+          torch.float8_e5m2: torch.float8_e4m3fn, torch.int16: torch.bfloat16}
+
+
+def copy_workspace(device="cuda"):
+    """A workspace for `copy`: its status stays at the first error until it is zeroed."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def _pool_desc(t, what):
+    """(descriptor, bytes of a page) of a (planes, pages, ...) CUDA tensor with contiguous pages."""
+    if not t.is_cuda or t.dim() < 3:
+        _fail(f"{what}: a CUDA tensor (planes, pages, ...)")
+    size, n = t.element_size(), 1
+    for d in range(t.dim() - 1, 1, -1):
+        if t.shape[d] != 1 and t.stride(d) != n:
+            _fail(f"{what}: pages are contiguous")
+        n *= t.shape[d]
+    # the stride of a dimension of one element says nothing
+    page = t.stride(1) * size if t.shape[1] > 1 else n * size
+    plane = t.stride(0) * size if t.shape[0] > 1 else page * t.shape[1]
+    return Z.PagePoolDesc(t.data_ptr(), plane, page, t.shape[0], t.shape[1]), n * size
+
+
+def _ids(v, device, what):
+    """A list of int32 numbers on the device; a Python sequence is copied there."""
+    if isinstance(v, torch.Tensor):
+        if v.dtype != torch.int32 or v.device != device or v.dim() != 1 or not v.is_contiguous():
+            _fail(f"{what}: a contiguous 1-D int32 tensor on {device}")
+        return v
+    return torch.tensor(list(v), dtype=torch.int32, device=device)
+
+
+def copy(src, src_ids, dst, dst_ids, count=None, ws=None, stream=None):
+    """Copy pages of src into dst (both (planes, pages, ...), of one page size): pair i from
+    page src_ids[i] to page dst_ids[i]; None for page i itself; negative numbers skip a pair.
+    Returns dst. Errors found on the device (zipnn_pages_copy) are in Z.status(ws); without
+    `ws` (copy_workspace) the call synchronises and raises them."""
+    if stream is not None:
+        with _use(stream, dst.device):
+            return copy(src, src_ids, dst, dst_ids, count, ws)
+    a, na = _pool_desc(src, "pages.copy: src")
+    b, nb = _pool_desc(dst, "pages.copy: dst")
+    if na != nb or src.device != dst.device or a.planes != b.planes:
+        _fail("pages.copy: src and dst have the same planes and page size, on one device")
+    if src_ids is not None:
+        src_ids = _ids(src_ids, dst.device, "pages.copy: src_ids")
+    if dst_ids is not None:
+        dst_ids = _ids(dst_ids, dst.device, "pages.copy: dst_ids")
+    n = min(v.numel() for v in (src_ids, dst_ids) if v is not None) if (src_ids is not None or dst_ids is not None) else min(a.pages, b.pages)
+    if src_ids is not None and dst_ids is not None and src_ids.numel() != dst_ids.numel():
+        _fail("pages.copy: as many destinations as sources")
+    if count is not None:
+        if not 0 <= count <= n:
+            _fail("pages.copy: count is at most the lists' length")
+        n = count
+    if n == 0 or na == 0 or a.planes == 0:
+        return dst
+    wait = ws is None
+    if wait:
+        ws = copy_workspace(dst.device)
+    _call(Z.zipnn_pages_copy, "zipnn_pages_copy", dst.device, ctypes.byref(a),
+          None if src_ids is None else src_ids.data_ptr(), ctypes.byref(b),
+          None if dst_ids is None else dst_ids.data_ptr(), n, na, ws.data_ptr(), ws.numel())
+    if wait:
+        with torch.cuda.device(dst.device):
+            Z.check(Z.status(ws), "pages.copy")
+    return dst
+
+
+class StoredPages:
+    """One sequence's pages as a container of the codec, and its length."""
+
+    def __init__(self, container, length, chunk_bytes):
+        self.container, self.length, self.chunk_bytes = container, length, chunk_bytes
+
+
+class PagePool:
+    """The pages of a cache and the sequences that hold them.
+
+    pages: CUDA tensor (planes, P, ...), each page contiguous and a multiple of 16 bytes.
+    max_seqs rows of max_pages slots. `meta` is one int32 tensor with refs (P), lens
+    (max_seqs) and tables (max_seqs x max_pages) one behind the other; given, it is taken as
+    it is (max_pages follows from its length), else it starts with every page free."""
+
+    def __init__(self, pages, page_tokens, max_seqs, max_pages=None, meta=None):
+        self._pool, self.page_bytes = _pool_desc(pages, "PagePool: pages")
+        P = pages.shape[1]
+        if not 1 <= max_seqs <= 1 << 18 or page_tokens < 1:
+            _fail("PagePool: 1 to 2^18 sequences, page_tokens at least 1")
+        if meta is None:
+            if max_pages is None or max_pages < 1 or max_seqs * max_pages >= 1 << 31:
+                _fail("PagePool: max_pages, at least 1 (max_seqs x max_pages below 2^31), or meta")
+            meta = torch.full((P + max_seqs * (1 + max_pages),), -1, dtype=torch.int32, device=pages.device)
+            meta[:P + max_seqs] = 0
+        slots = (meta.numel() - P - max_seqs) // max_seqs
+        if meta.dtype != torch.int32 or meta.device != pages.device or meta.dim() != 1 or not meta.is_contiguous() or \
+                slots < 1 or meta.numel() != P + max_seqs * (1 + slots) or (max_pages is not None and max_pages != slots):
+            _fail("PagePool: meta is int32, pages + max_seqs x (1 + max_pages) long, beside the pages")
+        self.pages, self.meta, self.page_tokens, self.device = pages, meta, page_tokens, pages.device
+        self.refs, self.lens = meta[:P], meta[P:P + max_seqs]
+        self.tables = meta[P + max_seqs:].view(max_seqs, slots)
+        self._table = Z.PageTableDesc(self.refs.data_ptr(), self.lens.data_ptr(), self.tables.data_ptr(), max_seqs, slots,
+                                      page_tokens)
+        self.ws = torch.zeros(Z.zipnn_pages_workspace_bytes(max_seqs, P), dtype=torch.uint8, device=pages.device)
+        self.live = self.ws[4:8].view(torch.int32)  # pages in use, as the last `compact` counted them
+
+    def fork(self, rows, parents, lens, stream=None):
+        """rows[j] becomes a sequence of lens[j] positions: new (parents[j] = -1), the start of
+        another row's, or the row itself grown (parents[j] = rows[j]); zipnn_pages_fork."""
+        if stream is not None:
+            with _use(stream, self.device):
+                return self.fork(rows, parents, lens)
+        rows, parents, lens = (_ids(v, self.device, "PagePool.fork") for v in (rows, parents, lens))
+        n = rows.numel()
+        if parents.numel() != n or lens.numel() != n or n > self._table.seqs:
+            _fail("PagePool.fork: a parent and a length for each row, each row at most once")
+        _call(Z.zipnn_pages_fork, "zipnn_pages_fork", self.device, ctypes.byref(self._pool), self.page_bytes,
+              ctypes.byref(self._table), rows.data_ptr(), parents.data_ptr(), lens.data_ptr(), n, self.ws.data_ptr(),
+              self.ws.numel())
+
+    def free(self, rows, compact=False, stream=None):
+        """The sequences in `rows` give their pages back; with compact, the gaps are closed
+        (zipnn_pages_free; `live` then holds how many pages are in use)."""
+        if stream is not None:
+            with _use(stream, self.device):
+                return self.free(rows, compact)
+        rows = _ids(rows, self.device, "PagePool.free")
+        _call(Z.zipnn_pages_free, "zipnn_pages_free", self.device, ctypes.byref(self._pool), self.page_bytes,
+              ctypes.byref(self._table), rows.data_ptr(), rows.numel(), int(compact), self.ws.data_ptr(), self.ws.numel())
+
+    def compact(self, stream=None):
+        """Close the gaps: afterwards the pages in use are the first `live` ones."""
+        self.free((), compact=True, stream=stream)
+
+    def gather(self, ids, out=None, stream=None):
+        """The pages `ids` as a contiguous (planes, len(ids), ...) tensor."""
+        if stream is not None:
+            with _use(stream, self.device):
+                return self.gather(ids, out)
+        ids = _ids(ids, self.device, "PagePool.gather")
+        if out is None:
+            out = torch.empty(self.pages.shape[:1] + ids.shape + self.pages.shape[2:], dtype=self.pages.dtype, device=self.device)
+        return copy(self.pages, ids, out, None, ids.numel(), self.ws)
+
+    def scatter(self, values, ids, stream=None):
+        """The pages of a (planes, len(ids), ...) tensor into the pages `ids`."""
+        copy(values, None, self.pages, ids, ws=self.ws, stream=stream)
+
+    def status(self, clear=False):
+        """The first error that a call on this pool found on the device since the status was
+        cleared (Z.OK if none); waits for the current stream."""
+        with torch.cuda.device(self.device):
+            s = Z.status(self.ws)
+        if clear:
+            self.ws[:4].zero_()
+        return s
+
+    def _held(self, row):
+        """(length, page numbers on the device) of a row; waits."""
+        if not 0 <= row < self._table.seqs:
+            _fail("PagePool: row out of range")
+        n = int(self.lens[row])
+        return n, self.tables[row, : -(-n // self.page_tokens)]
+
+    def store(self, row, chunk_bytes=Z.DEFAULT_CHUNK_BYTES, plan=None):
+        """The pages of the sequence in `row`, gathered and compressed (synchronises). The row
+        keeps them; free it to give them back."""
+        n, ids = self._held(row)
+        if n == 0:
+            _fail("PagePool.store: an empty row")
+        flat = self.gather(ids)
+        with torch.cuda.device(self.device):
+            c = Z.compress(flat.view(_CODEC.get(flat.dtype, flat.dtype)), chunk_bytes, plan)
+        return StoredPages(c, n, chunk_bytes)
+
+    def load(self, stored, row):
+        """A stored sequence back into the empty `row`, in fresh pages (synchronises)."""
+        before = self.status()
+        Z.check(before, "PagePool.load")
+        self.fork([row], [-1], [stored.length])
+        s = self.status(clear=True)
+        Z.check(s, "PagePool.load: no room")
+        _, ids = self._held(row)
+        dt = self.pages.dtype
+        shape = self.pages.shape[:1] + ids.shape + self.pages.shape[2:]
+        with torch.cuda.device(self.device):
+            flat = Z.decompress(stored.container, _CODEC.get(dt, dt), shape, stored.chunk_bytes)
+        self.scatter(flat.view(dt), ids)

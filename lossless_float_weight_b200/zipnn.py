@@ -91,6 +91,24 @@ zipnn_mx_scale_bytes = _sig("zipnn_mx_scale_bytes", _sz, _i, _u64, _u64)
 zipnn_mx_quantize = _sig("zipnn_mx_quantize", _i, _i, _i, _vp, _u64, _u64, _u64, _vp, _i, _vp, _vp, _vp, _sz, _vp)
 zipnn_mx_dequantize = _sig("zipnn_mx_dequantize", _i, _i, _i, _vp, _vp, _vp, _u64, _u64, _vp, _u64, _vp)
 
+
+
+class PagePoolDesc(ctypes.Structure):
+    """zipnn_page_pool: where the pages of a cache lie."""
+    _fields_ = [("base", _vp), ("plane_stride", _u64), ("page_stride", _u64), ("planes", _u32), ("pages", _u32)]
+
+
+class PageTableDesc(ctypes.Structure):
+    """zipnn_page_table: who holds them."""
+    _fields_ = [("refs", _vp), ("lens", _vp), ("tables", _vp), ("seqs", _u32), ("slots", _u32), ("page_tokens", _u32)]
+
+
+_pool_p, _table_p = ctypes.POINTER(PagePoolDesc), ctypes.POINTER(PageTableDesc)
+zipnn_pages_workspace_bytes = _sig("zipnn_pages_workspace_bytes", _sz, _u32, _u32)
+zipnn_pages_copy = _sig("zipnn_pages_copy", _i, _pool_p, _vp, _pool_p, _vp, _u32, _u64, _vp, _sz, _vp)
+zipnn_pages_fork = _sig("zipnn_pages_fork", _i, _pool_p, _u64, _table_p, _vp, _vp, _vp, _u32, _vp, _sz, _vp)
+zipnn_pages_free = _sig("zipnn_pages_free", _i, _pool_p, _u64, _table_p, _vp, _u32, _i, _vp, _sz, _vp)
+
 C_ABI_NAMES = [
     "zipnn_max_compressed_bytes", "zipnn_workspace_bytes", "zipnn_compress", "zipnn_compress_ex",
     "zipnn_decompress", "zipnn_compressed_size", "zipnn_get_status", "zipnn_histogram", "zipnn_code_lengths",
@@ -99,6 +117,7 @@ C_ABI_NAMES = [
     "zipnn_kernel_name", "zipnn_compress_noalloc", "zipnn_decompress_batch_workspace_bytes",
     "zipnn_decompress_batch", "zipnn_test_lookback_limit", "zipnn_shard_workspace_bytes", "zipnn_shard_sizes",
     "zipnn_shard_tables", "zipnn_mx_row_bytes", "zipnn_mx_scale_bytes", "zipnn_mx_quantize", "zipnn_mx_dequantize",
+    "zipnn_pages_workspace_bytes", "zipnn_pages_copy", "zipnn_pages_fork", "zipnn_pages_free",
 ]
 
 
