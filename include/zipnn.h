@@ -346,6 +346,21 @@ zipnn_status zipnn_mx_dequantize(zipnn_mx_format format, zipnn_value_type type, 
                                  const float* global_scale, uint64_t rows, uint64_t cols, void* out,
                                  uint64_t row_stride, zipnn_stream_t stream);
 
+/* out = A B^T for microscaled matrices of one format, A of m rows and B of n rows of k values:
+ * out (device, aligned to its values; row i at out + i * row_stride values) receives m rows of
+ * n. Products and scales are exact, sums are FP32 (the tensor cores' own), for NVFP4 times
+ * *a_global and *b_global, then rounded once to `type`. The order of a sum depends on the
+ * sizes alone, so equal calls give equal bits. A NaN scale makes its row's results NaN.
+ * At most 2^31 - 1 tiles of 128 x 128. Asynchronous, no workspace; a device-side wait that
+ * gives up (never expected) leaves its part of `out` unwritten and sets the device's status. */
+zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const void* a_scales, const float* a_global,
+                             const void* b_codes, const void* b_scales, const float* b_global, uint64_t m, uint64_t n,
+                             uint64_t k, zipnn_value_type type, void* out, uint64_t row_stride, zipnn_stream_t stream);
+
+/* Wait for `stream`, then return and clear what zipnn_mx_matmul calls on the current device
+ * set since this was last asked: ZIPNN_OK or ZIPNN_ERR_TIMEOUT. */
+zipnn_status zipnn_mx_status(zipnn_stream_t stream);
+
 /* ---- Pages of a K/V cache ------------------------------------------------------------
  * A served K/V cache lies in pages: page p of a pool holds `page_tokens` positions of one
  * sequence, in each of `planes` arrays (K and V of each layer). Sequences that start alike

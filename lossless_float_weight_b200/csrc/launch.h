@@ -11,7 +11,7 @@ bool device_ok();
 
 // Kernel ids of the optional event timing (timing.cu).
 enum KernelId { kIdHist = 0, kIdBuild, kIdLayout, kIdEncode, kIdDecode, kIdCodeLengths, kIdPlan, kIdShard, kIdPackHist, kIdPackEncode, kIdMxAmax,
-                kIdMxQuantize, kIdMxDequantize, kIdPagesPlan, kIdPagesMove, kNumKernelIds };
+                kIdMxQuantize, kIdMxDequantize, kIdMxMatmul, kIdPagesPlan, kIdPagesMove, kNumKernelIds };
 
 // Brackets one launch with CUDA events on `st` while timing is enabled.
 class TimedLaunch {

@@ -1,0 +1,409 @@
+// mx_matmul.cu -- the product of two microscaled 4-bit matrices (include/zipnn.h) on the
+// tensor cores: D = A B^T, the scales applied by the matrix instruction itself.
+//
+// One block computes 128 rows of one operand (P) against BN of the other (Q), over a range of
+// the columns, in stages of 256 columns: 128 bytes of codes a row, brought by TMA in the
+// 128-byte swizzle that tcgen05.mma reads, and the scales' 512-byte tiles, which lie in memory
+// as tcgen05.cp takes them. One thread feeds TMA, one issues the matrix instructions (K = 64
+// each, accumulating FP32 in tensor memory), four warps read the sums back and store them.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "zipnn.h"
+#include "bulk.cuh"
+#include "common.cuh"
+#include "launch.h"
+#include "mx.cuh"
+
+namespace zipnn {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr uint32_t kStageBytesK = 128;  // code bytes of a row in a stage: 256 values
+constexpr uint32_t kStageK = 256, kMmaK = 64;
+constexpr uint32_t kWaitPolls = 1u << 22;
+
+// ZIPNN_ERR_TIMEOUT after a wait that gave up, until zipnn_mx_status takes it.
+__device__ uint32_t g_mx_status;
+
+struct Args {
+  const uint8_t *p_scales, *q_scales;
+  const float *ga, *gb;  // the tensors' scales (NVFP4)
+  uint8_t* out;
+  uint64_t ldo;
+  uint32_t p_rows, q_rows, q_tiles;
+  uint32_t col_tiles;          // scale tiles along a row
+  uint32_t stages, mmas;       // of the whole row
+  uint32_t split;              // blocks of a cluster, each a range of the stages
+  int type, p_is_n;
+};
+
+template <int FMT, int BN>
+struct Shape {
+  static constexpr uint32_t kTiles = kStageK / (4 * mx_block(FMT));  // scale tiles of a stage along a row: 2 or 4
+  static constexpr uint32_t kHalves = BN > 128 ? 2 : 1;               // row tiles of Q's scales
+  static constexpr uint32_t kP = 128 * kStageBytesK, kQ = BN * kStageBytesK;
+  static constexpr uint32_t kSp = kTiles * kMxTileBytes, kSq = kSp * kHalves;
+  static constexpr uint32_t kStage = (kP + kQ + kSp + kSq + 1023) / 1024 * 1024;
+  static constexpr uint32_t kDepth = BN <= 64 ? 4 : BN == 128 ? 3 : 4;
+  static constexpr uint32_t kSmem = kDepth * kStage + 1024 + 256;
+  // Tensor memory: the sums, and a set of scales for each stage in shared memory (4 columns a
+  // tile), so that a set is written again only after the instructions that read it are done:
+  // the stage's codes were not brought before that either.
+  static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kHalves);
+  static constexpr uint32_t kUsed = BN + kDepth * kScaleCols;
+  static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+};
+
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                   smem_addr(dst)),
+               "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+               : "memory");
+}
+
+// Shared-memory descriptors: rows of 128 bytes in the 128-byte swizzle (groups of 8 rows 1024
+// bytes apart), and unswizzled 16-byte rows (groups of 8 rows 128 bytes apart).
+__device__ __forceinline__ uint64_t desc_codes(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t addr) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc_scales(addr)) : "memory");
+}
+
+// Which two of a column's four scale bytes an MXFP4 instruction takes is part of its
+// descriptor; an NVFP4 instruction takes all four.
+template <int FMT, int BN>
+__device__ __forceinline__ constexpr uint32_t instr(uint32_t scale_id) {
+  return scale_id << 4 | 1u << 7 | 1u << 10 | (uint32_t)(BN / 8) << 17 | (FMT == kMxFp4 ? 1u : 0u) << 23 | 1u << 27 | scale_id << 29;
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
+  if constexpr (FMT == kMxFp4) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+  }
+}
+
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void load_sums(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float load_peer(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store(const Args& a, uint32_t p, uint32_t q, float v, float g0, float g1) {
+  if (p >= a.p_rows || q >= a.q_rows) return;
+  v = v * g0 * g1;
+  const uint64_t at = a.p_is_n ? (uint64_t)q * a.ldo + p : (uint64_t)p * a.ldo + q;
+  if (a.type == kValFP32) reinterpret_cast<float*>(a.out)[at] = v;
+  else if (a.type == kValBF16) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+  else reinterpret_cast<__half*>(a.out)[at] = __float2half_rn(v);
+}
+
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ CUtensorMap p_map,
+                                                        const __grid_constant__ CUtensorMap q_map, const Args a) {
+  using S = Shape<FMT, BN>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kDepth * S::kStage);
+  uint64_t *empty = full + S::kDepth, *done = empty + S::kDepth;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
+  volatile uint32_t* failed = tmem_at + 1;
+
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t tile = blockIdx.x / a.split, rank = blockIdx.x % a.split;
+  const uint32_t p0 = tile / a.q_tiles * 128, q0 = tile % a.q_tiles * BN;
+  const uint32_t lo = (uint32_t)((uint64_t)a.stages * rank / a.split), hi = (uint32_t)((uint64_t)a.stages * (rank + 1) / a.split);
+
+  if (warp == 4 && lane == 0) {
+    for (uint32_t i = 0; i < S::kDepth; i++) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(done, 1);
+    *failed = 0;
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_at)), "r"(S::kCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_at);
+
+  if (warp == 4) {
+    if (lane == 0) {
+      for (uint32_t i = lo; i < hi; i++) {
+        const uint32_t n = i - lo, s = n % S::kDepth;
+        if (n >= S::kDepth && !mbar_wait_bounded(empty + s, (n / S::kDepth - 1) & 1, kWaitPolls)) {
+          *failed = 1;
+          break;
+        }
+        uint8_t* st = smem + s * S::kStage;
+        const uint32_t t0 = i * S::kTiles, bytes = min(S::kTiles, a.col_tiles - t0) * kMxTileBytes;
+        const uint32_t halves = S::kHalves == 2 && q0 + 128 < a.q_rows ? 2 : 1;
+        mbar_expect_tx(full + s, S::kP + S::kQ + bytes * (1 + halves));
+        tma_2d(st, &p_map, (int32_t)(i * kStageBytesK), (int32_t)p0, full + s);
+        tma_2d(st + S::kP, &q_map, (int32_t)(i * kStageBytesK), (int32_t)q0, full + s);
+        uint8_t* sc = st + S::kP + S::kQ;
+        bulk_g2s(sc, a.p_scales + ((uint64_t)(p0 / 128) * a.col_tiles + t0) * kMxTileBytes, bytes, full + s);
+        for (uint32_t h = 0; h < halves; h++)
+          bulk_g2s(sc + S::kSp + h * S::kSp, a.q_scales + ((uint64_t)(q0 / 128 + h) * a.col_tiles + t0) * kMxTileBytes, bytes, full + s);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0) {
+      for (uint32_t i = lo; i < hi; i++) {
+        const uint32_t n = i - lo, s = n % S::kDepth;
+        if (!mbar_wait_bounded(full + s, (n / S::kDepth) & 1, kWaitPolls)) {
+          *failed = 1;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t st = smem_addr(smem + s * S::kStage), sc = st + S::kP + S::kQ;
+        const uint32_t tp = tmem + BN + s * S::kScaleCols, tq = tp + 4 * S::kTiles;
+        const uint32_t tiles = min(S::kTiles, a.col_tiles - i * S::kTiles);
+        for (uint32_t t = 0; t < tiles; t++) {
+          copy_scales(tp + 4 * t, sc + t * kMxTileBytes);
+          for (uint32_t h = 0; h < S::kHalves; h++)
+            copy_scales(tq + 4 * (t * S::kHalves + h), sc + S::kSp + h * S::kSp + t * kMxTileBytes);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kStageK / kMmaK; k++) {
+          if (i * (kStageK / kMmaK) + k >= a.mmas) break;
+          const uint32_t t = FMT == kMxFp4 ? k / 2 : k, id = FMT == kMxFp4 ? k % 2 * 2 : 0;
+          mma<FMT>(tmem, desc_codes(st + k * 32), desc_codes(st + S::kP + k * 32), instr<FMT, BN>(id), tp + 4 * t,
+                   tq + 4 * t * S::kHalves, n + k > 0);
+        }
+        commit(empty + s);
+      }
+      commit(done);
+    }
+    __syncwarp();
+  } else {
+    if (!mbar_wait_bounded(done, 0, kWaitPolls)) *failed = 1;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  }
+  __syncthreads();
+  if (*failed) {
+    if (threadIdx.x == 0) atomicMax(&g_mx_status, kStTimeout);
+  }
+  const bool ok = *failed == 0;
+  const float g0 = FMT == kNvFp4 ? *a.ga : 1.f, g1 = FMT == kNvFp4 ? *a.gb : 1.f;
+  if (a.split == 1) {
+    if (warp < 4 && ok) {
+      for (uint32_t c = 0; c < (uint32_t)BN; c += 16) {
+        if (q0 + c >= a.q_rows) break;
+        float v[16];
+        load_sums(tmem + (warp * 32 << 16) + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; i++) store(a, p0 + threadIdx.x, q0 + c + i, v[i], g0, g1);
+      }
+    }
+  } else {
+    // each block's sums to its shared memory (its stages are spent), then every block adds its
+    // share of the columns over the cluster, in the blocks' order
+    float* sums = reinterpret_cast<float*>(smem);
+    if (warp < 4) {
+      for (uint32_t c = 0; c < (uint32_t)BN; c += 16) {
+        float v[16];
+        load_sums(tmem + (warp * 32 << 16) + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; i++) sums[(c + i) * 128 + threadIdx.x] = v[i];
+      }
+    }
+    cluster_sync();
+    if (warp < 4 && ok) {
+      for (uint32_t c = rank; c < (uint32_t)BN && q0 + c < a.q_rows; c += a.split) {
+        float v = 0.f;
+        for (uint32_t r = 0; r < a.split; r++) v += load_peer(peer(smem_addr(sums + c * 128 + threadIdx.x), r));
+        store(a, p0 + threadIdx.x, q0 + c, v, g0, g1);
+      }
+    }
+    cluster_sync();
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 5) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols));
+  }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static std::atomic<void*> cached{nullptr};
+  void* f = cached.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    cached.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
+}
+
+// Codes as rows of bytes, a box of 128 bytes x `box` rows; zeros outside.
+bool code_map(CUtensorMap* m, const void* codes, uint64_t rows, uint64_t row_bytes, uint32_t box) {
+  EncodeTiled f = encode_tiled();
+  const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
+  const cuuint32_t boxes[2] = {kStageBytesK, box}, steps[2] = {1, 1};
+  return f && f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, boxes, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operand {
+  const void* codes;
+  const uint8_t* scales;
+  uint64_t rows;
+};
+
+template <int FMT, int BN>
+cudaError_t launch_tiles(const Operand& p, const Operand& q, uint64_t cols, Args a, cudaStream_t st) {
+  using S = Shape<FMT, BN>;
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(k_mx_matmul<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  CUtensorMap pm, qm;
+  const uint64_t rb = mx_row_bytes(cols);
+  if (!code_map(&pm, p.codes, p.rows, rb, 128) || !code_map(&qm, q.codes, q.rows, rb, BN)) return cudaErrorUnknown;
+  const uint64_t q_tiles = mx_div_up(q.rows, BN), tiles = mx_div_up(p.rows, 128) * q_tiles;
+  a.q_tiles = (uint32_t)q_tiles;
+  a.split = 1;
+  while (a.split < 8 && tiles * a.split * 2 <= 2 * 148 && a.split * 2 <= a.stages) a.split *= 2;
+  if (tiles * a.split > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((uint32_t)(tiles * a.split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  TimedLaunch t(kIdMxMatmul, st);
+  return cudaLaunchKernelEx(&cfg, k_mx_matmul<FMT, BN>, pm, qm, a);
+}
+
+template <int FMT>
+cudaError_t launch_matmul(const Operand& p, const Operand& q, uint64_t cols, const Args& a, cudaStream_t st) {
+  if (q.rows <= 16) return launch_tiles<FMT, 16>(p, q, cols, a, st);
+  if (q.rows <= 32) return launch_tiles<FMT, 32>(p, q, cols, a, st);
+  if (q.rows <= 64) return launch_tiles<FMT, 64>(p, q, cols, a, st);
+  return launch_tiles<FMT, 128>(p, q, cols, a, st);
+}
+
+inline bool off16(const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+}  // namespace
+}  // namespace zipnn
+
+using namespace zipnn;
+
+extern "C" {
+
+zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const void* a_scales, const float* a_global,
+                             const void* b_codes, const void* b_scales, const float* b_global, uint64_t m, uint64_t n,
+                             uint64_t k, zipnn_value_type type, void* out, uint64_t row_stride, zipnn_stream_t stream) {
+  if (!mx_valid(format, m, k) || !mx_valid(format, n, k) || !mx_valid_type(type)) return ZIPNN_ERR_INVALID_ARG;
+  if (off16(a_codes) || off16(a_scales) || off16(b_codes) || off16(b_scales) || !out) return ZIPNN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(out) % mx_value_bytes(type) || row_stride < n || row_stride > kMxMaxCols) return ZIPNN_ERR_INVALID_ARG;
+  if (format == ZIPNN_NVFP4 && (!a_global || !b_global || reinterpret_cast<uintptr_t>(a_global) % 4 || reinterpret_cast<uintptr_t>(b_global) % 4))
+    return ZIPNN_ERR_INVALID_ARG;
+  if (mx_div_up(m, 128) * mx_div_up(n, 128) > 0x7FFFFFFFull) return ZIPNN_ERR_INVALID_ARG;
+  if (!device_ok()) return ZIPNN_ERR_UNSUPPORTED;
+  // the longer side lies along the 128 rows of a block
+  const bool p_is_n = n >= m;
+  const Operand a{a_codes, static_cast<const uint8_t*>(a_scales), m}, b{b_codes, static_cast<const uint8_t*>(b_scales), n};
+  const Operand &p = p_is_n ? b : a, &q = p_is_n ? a : b;
+  Args g = {};
+  g.p_scales = p.scales;
+  g.q_scales = q.scales;
+  g.ga = a_global;
+  g.gb = b_global;
+  g.out = static_cast<uint8_t*>(out);
+  g.ldo = row_stride;
+  g.p_rows = (uint32_t)p.rows;
+  g.q_rows = (uint32_t)q.rows;
+  g.col_tiles = (uint32_t)mx_col_tiles(format, k);
+  g.stages = (uint32_t)mx_div_up(k, kStageK);
+  g.mmas = (uint32_t)mx_div_up(k, kMmaK);
+  g.type = type;
+  g.p_is_n = p_is_n;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = format == ZIPNN_MXFP4 ? launch_matmul<kMxFp4>(p, q, k, g, st) : launch_matmul<kNvFp4>(p, q, k, g, st);
+  return e == cudaSuccess ? ZIPNN_OK : ZIPNN_ERR_CUDA;
+}
+
+zipnn_status zipnn_mx_status(zipnn_stream_t stream) {
+  if (!device_ok()) return ZIPNN_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  const uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_mx_status, 4, 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbolAsync(g_mx_status, &zero, 4, 0, cudaMemcpyHostToDevice, st);
+  return e == cudaSuccess ? (zipnn_status)v : ZIPNN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -12,8 +12,8 @@ namespace {
 
 const char* const kNames[kNumKernelIds] = {"split_hist", "code_build", "layout_scan", "encode",
                                            "decode_merge", "code_lengths", "plan", "shard_tables",
-                                           "pack_hist", "pack_encode", "mx_amax", "mx_quantize", "mx_dequantize", "pages_plan",
-                                           "pages_move"};
+                                           "pack_hist", "pack_encode", "mx_amax", "mx_quantize", "mx_dequantize", "mx_matmul",
+                                           "pages_plan", "pages_move"};
 
 struct Pending {
   int id;

@@ -1,4 +1,4 @@
-"""Microscaled 4-bit tensors: made, read back, and stored compressed.
+"""Microscaled 4-bit tensors: made, read back, multiplied, and stored compressed.
 
 A matrix of E2M1 values whose blocks share a scale ("mxfp4": 32 values, E8M0 scales;
 "nvfp4": 16 values, E4M3 scales and one FP32 scale of the tensor), in the layout of
@@ -7,6 +7,7 @@ quantised weight or K/V cache goes through :func:`compress` and comes back bit f
 
     q = mx.quantize(w)                  # w: (..., K) BF16, FP16 or FP32
     w4 = mx.dequantize(q)               # BF16 values
+    y = mx.matmul(x, q)                 # x (..., K), quantised alike, against the weight
     c = mx.compress(q)                  # two containers of the codec
     q2 = mx.decompress(c)               # the same codes and scales
 
@@ -178,6 +179,35 @@ def dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
         _call(Z.zipnn_mx_dequantize, "zipnn_mx_dequantize", q.device, _FORMATS[q.format], _VALUES[dtype],
               q.codes.data_ptr(), q.scales.data_ptr(), q._global, q.rows, q.cols, out.data_ptr(), stride)
     return out
+
+
+def matmul(a, b, dtype=torch.bfloat16, out=None, stream=None):
+    """a @ b.T for a (..., K) and b (N, K) of one format, FP32 sums, as BF16, FP16 or FP32
+    (..., N). a may be a BF16, FP16 or FP32 tensor: it is then quantised in b's format first
+    (activations against a quantised weight); see zipnn_mx_matmul."""
+    if stream is not None:
+        with _use(stream, b.device):
+            return matmul(a, b, dtype, out)
+    if not isinstance(b, MxTensor):
+        _fail("mx.matmul: b is an MxTensor")
+    if not isinstance(a, MxTensor):
+        a = quantize(a, b.format)
+    if a.format != b.format or a.cols != b.cols or len(b.shape) != 2 or a.device != b.device or dtype not in _VALUES:
+        _fail("mx.matmul: a (..., K) and b (N, K) of one format, on one device, to BF16, FP16 or FP32")
+    out = _out(out, a.shape[:-1] + (b.rows,), dtype, a.device, "mx.matmul")
+    if a.rows and b.rows:
+        stride = out.stride(0) if out.dim() == 2 and a.rows > 1 else b.rows
+        _call(Z.zipnn_mx_matmul, "zipnn_mx_matmul", a.device, _FORMATS[a.format], a.codes.data_ptr(), a.scales.data_ptr(),
+              a._global, b.codes.data_ptr(), b.scales.data_ptr(), b._global, a.rows, b.rows, a.cols, _VALUES[dtype],
+              out.data_ptr(), stride)
+    return out
+
+
+def status(device=None):
+    """Z.OK, or Z.ERR_TIMEOUT if a product on the device gave up since this was last asked
+    (waits for the current stream)."""
+    with torch.cuda.device(device):
+        return Z.zipnn_mx_status(torch.cuda.current_stream().cuda_stream)
 
 
 class MxContainers:

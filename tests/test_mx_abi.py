@@ -43,7 +43,17 @@ def test_argument_errors_without_a_device(Z):
     for bad in (dict(fmt=-1), dict(t=9), dict(codes=None), dict(codes=fake + 1), dict(scales=None), dict(g=None),
                 dict(rows=0), dict(cols=0), dict(out=None), dict(out=fake + 1), dict(stride=10)):
         assert deq(**bad) == Z.ERR_INVALID_ARG, bad
+    def matmul(fmt=Z.NVFP4, ac=fake, asc=fake, ag=fake, bc=fake, bsc=fake, bg=fake, m=4, n=8, k=64, t=Z.VALUE_BF16, out=fake,
+               stride=8):
+        return Z.zipnn_mx_matmul(fmt, ac, asc, ag, bc, bsc, bg, m, n, k, t, out, stride, None)
+
+    for bad in (dict(fmt=2), dict(ac=None), dict(asc=fake + 8), dict(ag=None), dict(bc=fake + 4), dict(bsc=None), dict(bg=fake + 1),
+                dict(m=0), dict(n=0), dict(k=0), dict(t=5), dict(out=None), dict(out=fake + 1), dict(stride=7),
+                dict(m=1 << 31, n=1 << 31, stride=1 << 31)):
+        assert matmul(**bad) == Z.ERR_INVALID_ARG, bad
     if not torch.cuda.is_available():
+        assert matmul() == Z.ERR_UNSUPPORTED and matmul(fmt=Z.MXFP4, ag=None, bg=None) == Z.ERR_UNSUPPORTED
+        assert Z.zipnn_mx_status(None) == Z.ERR_UNSUPPORTED
         assert quant() == Z.ERR_UNSUPPORTED and deq() == Z.ERR_UNSUPPORTED
         assert quant(fmt=Z.MXFP4, g=None, w=None, wb=0) == Z.ERR_UNSUPPORTED  # not needed for MXFP4
 
