@@ -15,37 +15,56 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kMaxPartials = ZIPNN_MX_WORKSPACE_BYTES / 4;
-constexpr int kChunk = 16;  // values of one thread: 8 bytes of codes
+constexpr int kChunk = 32;    // values that one thread quantises: 16 bytes of codes
+constexpr int kReadBack = 16;  // values that one thread reads back: 8 bytes of codes, 32 or 64 of values
 
-// Threads of a block cover `rows_per` rows x `chunk_cols` (a power of two) chunks.
+// How a grid covers rows x chunks (chunks: what one thread takes of a row): a block takes a
+// power of two of chunks of as many rows as its threads reach, and walks down the rows at a
+// fixed distance, so that a thread's columns, and all that follows from them, are settled once.
 struct Cover {
-  uint32_t log_cols;   // log2 of chunk_cols
-  uint32_t col_tiles;  // blocks of chunks along a row
-  uint64_t tiles;
+  uint32_t log_cols;   // log2 of the chunks of a block
+  uint32_t col_tiles;  // blocks beside each other along a row
+  uint32_t row_tiles;  // blocks (at different times) below each other
+  uint32_t grid;       // col_tiles x the blocks that walk down
 };
 
-Cover cover(uint64_t rows, uint64_t chunks) {
+Cover cover(uint64_t rows, uint64_t chunks, uint32_t most) {
   Cover c;
   c.log_cols = 0;
   while ((1ull << c.log_cols) < chunks && (1 << c.log_cols) < kThreads) c.log_cols++;
   c.col_tiles = (uint32_t)mx_div_up(chunks, 1ull << c.log_cols);
-  c.tiles = mx_div_up(rows, (uint64_t)kThreads >> c.log_cols) * c.col_tiles;
+  c.row_tiles = (uint32_t)mx_div_up(rows, (uint64_t)kThreads >> c.log_cols);
+  const uint32_t down = most / c.col_tiles;
+  c.grid = c.col_tiles * (down < 1 ? 1 : down < c.row_tiles ? down : c.row_tiles);
   return c;
 }
 
-__device__ __forceinline__ void place(const Cover& c, uint64_t tile, uint64_t& row, uint32_t& chunk) {
-  const uint64_t rt = tile / c.col_tiles;
-  const uint32_t ct = (uint32_t)(tile - rt * c.col_tiles);
-  row = rt * (kThreads >> c.log_cols) + (threadIdx.x >> c.log_cols);
-  chunk = (ct << c.log_cols) + (threadIdx.x & ((1u << c.log_cols) - 1));
-}
+struct Walk {
+  uint32_t chunk;      // this thread's, along a row
+  uint32_t tile;       // row tile of the block
+  uint32_t tile_step;
+  uint32_t sub, per;   // this thread's row in a tile, rows of a tile
+  // The blocks stand `across` beside each other; `ct`: the column tile of this one.
+  __device__ __forceinline__ Walk(const Cover& c, uint32_t across, uint32_t ct) {
+    tile = blockIdx.x / across;
+    tile_step = gridDim.x / across;
+    chunk = (ct << c.log_cols) + (threadIdx.x & ((1u << c.log_cols) - 1));
+    sub = threadIdx.x >> c.log_cols;
+    per = kThreads >> c.log_cols;
+  }
+  __device__ __forceinline__ explicit Walk(const Cover& c) : Walk(c, c.col_tiles, blockIdx.x % c.col_tiles) {}
+  __device__ __forceinline__ uint32_t row() const { return tile * per + sub; }
+};
 
 struct Matrix {
   const uint8_t* base;
   const uint8_t* end;  // past the last row's last value
-  uint64_t rows, stride_bytes;
-  uint32_t cols;
+  uint64_t stride_bytes;
+  uint32_t rows, cols;
 };
+
+template <int TYPE>
+constexpr int kWords = kChunk * (int)mx_value_bytes(TYPE) / 4;
 
 template <int TYPE>
 __device__ __forceinline__ float value_at(const uint8_t* p) {
@@ -54,64 +73,103 @@ __device__ __forceinline__ float value_at(const uint8_t* p) {
   return __half2float(*reinterpret_cast<const __half*>(p));
 }
 
-// Values 16 * chunk .. 16 * chunk + 15 of a row, zeros past its end. Whole 16-byte vectors
-// around them are loaded where they lie inside the matrix, whatever the row's own alignment
-// (a row of odd length starts anywhere), and shifted into place; the matrix's first and last
-// bytes are read value by value.
-template <int TYPE>
-__device__ __forceinline__ void load_chunk(const Matrix& m, uint64_t row, uint32_t chunk, float (&v)[kChunk]) {
-  constexpr int B = (int)mx_value_bytes(TYPE), W = kChunk * B / 4;
+// The values 32 * chunk .. 32 * chunk + 31 of a row, as they lie in memory (FP32: a word each,
+// else two to a word), zeros past its end. ALIGNED: every row starts on a 32-byte boundary, and
+// 32-byte vectors are loaded; else (a row of odd length starts anywhere) 16-byte vectors around
+// the values, shifted into place. What of this would leave the matrix's memory is read value
+// by value.
+template <int TYPE, bool ALIGNED>
+__device__ __forceinline__ void load_chunk(const Matrix& m, uint32_t row, uint32_t chunk, uint32_t (&w)[kWords<TYPE>]) {
+  constexpr int B = (int)mx_value_bytes(TYPE), W = kWords<TYPE>;
   const uint32_t first = chunk * kChunk;
   if (row >= m.rows || first >= m.cols) {
 #pragma unroll
-    for (int i = 0; i < kChunk; i++) v[i] = 0.f;
+    for (int i = 0; i < W; i++) w[i] = 0;
     return;
   }
   const uint8_t* p = m.base + row * m.stride_bytes + (uint64_t)first * B;
-  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+  const uint32_t off = ALIGNED ? 0 : (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
   const uint8_t* a = p - off;
   const uint32_t left = m.cols - first;
-  if (a >= m.base && a + W * 4 + (off ? 16 : 0) <= m.end) {
-    uint32_t w[W + 4];
+  if ((ALIGNED || a >= m.base) && a + W * 4 + (off ? 16 : 0) <= m.end) {
+    if constexpr (ALIGNED) {
 #pragma unroll
-    for (int i = 0; i < W / 4; i++) {
-      const uint4 t = __ldg(reinterpret_cast<const uint4*>(a) + i);
-      w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
-    }
-    if (off) {
-      const uint4 t = __ldg(reinterpret_cast<const uint4*>(a) + W / 4);
-      w[W] = t.x, w[W + 1] = t.y, w[W + 2] = t.z, w[W + 3] = t.w;
-      if (off & 8) {
+      for (int i = 0; i < W / 8; i++) ld_nc_v8(a + 32 * i, w + 8 * i);
+    } else {
+      uint32_t t[W + 4];
 #pragma unroll
-        for (int i = 0; i < W + 2; i++) w[i] = w[i + 2];
+      for (int i = 0; i < W / 4; i++) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a) + i);
+        t[4 * i] = v.x, t[4 * i + 1] = v.y, t[4 * i + 2] = v.z, t[4 * i + 3] = v.w;
       }
-      if (off & 4) {
+      if (off) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a) + W / 4);
+        t[W] = v.x, t[W + 1] = v.y, t[W + 2] = v.z, t[W + 3] = v.w;
+        if (off & 8) {
 #pragma unroll
-        for (int i = 0; i < W + 1; i++) w[i] = w[i + 1];
-      }
-      if (off & 2) {
+          for (int i = 0; i < W + 2; i++) t[i] = t[i + 2];
+        }
+        if (off & 4) {
 #pragma unroll
-        for (int i = 0; i < W; i++) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-      }
-    }
+          for (int i = 0; i < W + 1; i++) t[i] = t[i + 1];
+        }
+        if (off & 2) {
 #pragma unroll
-    for (int i = 0; i < kChunk; i++) {
-      if constexpr (TYPE == kValFP32) {
-        v[i] = __uint_as_float(w[i]);
-      } else if constexpr (TYPE == kValBF16) {
-        v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-      } else {
-        v[i] = __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (i & 1 ? 16 : 0))));
+          for (int i = 0; i < W; i++) t[i] = __funnelshift_r(t[i], t[i + 1], 16);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < W; i++) w[i] = t[i];
     }
     if (left < kChunk) {
 #pragma unroll
-      for (int i = 0; i < kChunk; i++) v[i] = (uint32_t)i < left ? v[i] : 0.f;
+      for (int i = 0; i < W; i++) {
+        if constexpr (B == 4) w[i] = (uint32_t)i < left ? w[i] : 0;
+        else w[i] = 2u * i + 1 < left ? w[i] : 2u * i < left ? w[i] & 0xFFFF : 0;
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kChunk; i++) v[i] = (uint32_t)i < left ? value_at<TYPE>(p + i * B) : 0.f;
+    for (int i = 0; i < W; i++) {
+      if constexpr (B == 4) {
+        w[i] = (uint32_t)i < left ? reinterpret_cast<const uint32_t*>(p)[i] : 0;
+      } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+        w[i] = (2u * i < left ? h[2 * i] : 0u) | (2u * i + 1 < left ? (uint32_t)h[2 * i + 1] << 16 : 0u);
+      }
+    }
   }
+}
+
+// Value i of a chunk.
+template <int TYPE>
+__device__ __forceinline__ float value_of(const uint32_t (&w)[kWords<TYPE>], int i) {
+  if constexpr (TYPE == kValFP32) return __uint_as_float(w[i]);
+  if constexpr (TYPE == kValBF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  return __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> (i & 1 ? 16 : 0))));
+}
+
+// The largest magnitude among `n` values from value `from` of a chunk, as an integer of the
+// type's own width (so that a NaN is above every number), and that integer as the bits of an
+// FP32 value (infinite or more: not finite).
+template <int TYPE>
+__device__ __forceinline__ uint32_t chunk_top(const uint32_t (&w)[kWords<TYPE>], int from, int n) {
+  uint32_t t = 0;
+  if constexpr (TYPE == kValFP32) {
+#pragma unroll
+    for (int i = from; i < from + n; i++) t = max(t, w[i] & 0x7FFFFFFF);
+    return t;
+  } else {
+#pragma unroll
+    for (int i = from / 2; i < (from + n) / 2; i += 2) t = __vimax3_u16x2(t, w[i] & 0x7FFF7FFF, w[i + 1] & 0x7FFF7FFF);
+    return max(t >> 16, t & 0xFFFF);
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t top_bits(uint32_t t) {
+  if constexpr (TYPE == kValFP32) return t;
+  if constexpr (TYPE == kValBF16) return t << 16;
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)t)));
 }
 
 // Two FP32 quotients to a byte of two E2M1 codes (the first in the low nibble), four such
@@ -154,43 +212,75 @@ __device__ __forceinline__ uint32_t nv_scale(float amax, float g, float inv6g) {
   return to_e4m3(t);
 }
 
-// The codes of a block's values for the scale s g. q = x * (1 / (s g)) is off by less than 4
-// of its last steps; a quotient within that of a border between two E2M1 values (its low 21
-// fraction bits are then near 0) sends the thread to the comparison of |x| with the seven
-// borders times s g, which is exact: border * s has 7 bits, and its product with g rounded
-// up or down separates |x| >= border from |x| > border.
-__device__ __forceinline__ void nv_codes(const float (&v)[kChunk], float s, float g, uint32_t (&codes)[2]) {
-  const float unit = s * g;
-  if (s == 0.f) {
-    float z[kChunk];
+// The codes of 16 values for a unit s g out of the range of nv_codes: |x| against the seven
+// borders between codes times s g. border * s has 7 bits, and its product with g rounded up or
+// down separates >= from >.
+__device__ __noinline__ uint2 nv_codes_any(const float* v, float s, float g) {
+  const float border[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.f};
+  uint32_t codes[2] = {0, 0};
+  for (int i = 0; i < 16; i++) {
+    const float x = fabsf(v[i]);
+    uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < kChunk; i++) z[i] = copysignf(0.f, v[i]);
-    codes[0] = to_e2m1(z), codes[1] = to_e2m1(z + 8);
-    return;
+    for (int k = 0; k < 7; k++) c += k & 1 ? x >= __fmul_ru(border[k] * s, g) : x > __fmul_rd(border[k] * s, g);
+    c |= __float_as_uint(v[i]) >> 31 << 3;
+    codes[i / 8] |= c << (4 * (i % 8));
   }
-  const float inv = __frcp_rn(unit);
-  float q[kChunk];
-  uint32_t near = 0xFFFFFFFFu;
+  return make_uint2(codes[0], codes[1]);
+}
+
+// Which of two neighbouring codes, `low` and the next, is nearest to x / (s g) (the even one
+// where it lies on their border m): the sign of
+//   |x| - m s g = (|x| - m u) - m e,  u = s g rounded, e = s g - u,
+// where e is exact (s has 4 bits, g 24), and so is |x| - m u (a few bits left of a difference
+// between neighbours), so that the last rounding keeps the sign.
+__device__ __forceinline__ uint32_t nv_between(uint32_t low, float x, float u, float e) {
+  const float m = low < 4 ? (float)(2 * low + 1) * 0.25f : low == 4 ? 2.5f : low == 5 ? 3.5f : 5.f;
+  const float d = fmaf(-m, e, fmaf(-m, u, fabsf(x)));
+  return d > 0.f || (d == 0.f && (low & 1)) ? low + 1 : low;
+}
+
+// The codes of a block's 16 values for the scale s g. 1 / (s g) is known to 1.5 of its last
+// steps, so each quotient is taken with a factor a little below and one a little above it
+// (2^-21 of it): where both round to the same code, that is the code. The few values so near
+// to a border that they do not (with a scale found from BF16 values about one in 400, since
+// quotients of few bits meet there) are read again, one by one, and settled exactly.
+template <int TYPE>
+__device__ __forceinline__ void nv_codes(const uint32_t (&w)[kWords<TYPE>], int from, const uint8_t* at, float s, float g,
+                                         uint32_t* codes) {
+  const float u = s * g;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(u));
+  if (s == 0.f) inv = 0.f;
+  const float below = inv * (1.f - 0x1p-21f), above = inv * (1.f + 0x1p-21f);
+  uint32_t other[2];
+  {
+    float q[16], r[16];
 #pragma unroll
-  for (int i = 0; i < kChunk; i++) {
-    q[i] = v[i] * inv;
-    near = min(near, (__float_as_uint(q[i]) + 4) & 0x1FFFFF);
+    for (int i = 0; i < 16; i++) {
+      const float x = value_of<TYPE>(w, from + i);
+      q[i] = x * below, r[i] = x * above;
+    }
+    codes[0] = to_e2m1(q), codes[1] = to_e2m1(q + 8);
+    other[0] = to_e2m1(r), other[1] = to_e2m1(r + 8);
   }
-  codes[0] = to_e2m1(q), codes[1] = to_e2m1(q + 8);
-  if (near < 8 || !(unit >= 1e-30f && unit <= 1e30f)) {
-    const float border[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.f};
-    float t[7];
+  if (!(s == 0.f || (u >= 1e-30f && u <= 1e30f))) {
+    float v[16];
 #pragma unroll
-    for (int k = 0; k < 7; k++) t[k] = k & 1 ? __fmul_ru(border[k] * s, g) : __fmul_rd(border[k] * s, g);
-    codes[0] = codes[1] = 0;
+    for (int i = 0; i < 16; i++) v[i] = value_of<TYPE>(w, from + i);
+    const uint2 c = nv_codes_any(v, s, g);
+    codes[0] = c.x, codes[1] = c.y;
+  } else if ((codes[0] ^ other[0]) | (codes[1] ^ other[1])) {
+    const float e = fmaf(s, g, -u);
 #pragma unroll
-    for (int i = 0; i < kChunk; i++) {
-      const float x = fabsf(v[i]);
-      uint32_t c = 0;
-#pragma unroll
-      for (int k = 0; k < 7; k++) c += k & 1 ? x >= t[k] : x > t[k];
-      c |= __float_as_uint(v[i]) >> 31 << 3;
-      codes[i / 8] |= c << (4 * (i % 8));
+    for (int h = 0; h < 2; h++) {
+      uint32_t diff = codes[h] ^ other[h];
+      while (diff) {
+        const uint32_t i = (uint32_t)(__ffs(diff) - 1) / 4, low = codes[h] >> (4 * i) & 7;
+        const uint32_t c = nv_between(low, value_at<TYPE>(at + (8 * h + i) * mx_value_bytes(TYPE)), u, e);
+        codes[h] += (c - low) << (4 * i);
+        diff &= ~(15u << (4 * i));
+      }
     }
   }
 }
@@ -204,33 +294,45 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* smem) {
 }
 
 // The largest finite magnitude of each block's share of the matrix, to partial[blockIdx.x].
-template <int TYPE>
+template <int TYPE, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) k_mx_amax(Matrix m, Cover c, uint32_t* partial) {
   __shared__ uint32_t smem[kThreads / 32];
   uint32_t top = 0;
-  for (uint64_t t = blockIdx.x; t < c.tiles; t += gridDim.x) {
-    uint64_t row;
-    uint32_t chunk;
-    place(c, t, row, chunk);
-    float v[kChunk];
-    load_chunk<TYPE>(m, row, chunk, v);
+  constexpr int kAhead = TYPE == kValFP32 ? 1 : 2;  // rows in flight: 128 bytes a thread
+  const uint32_t across = min(c.col_tiles, gridDim.x);  // fewer than the columns need where a row alone fills the grid
+  for (uint32_t ct = blockIdx.x % across; ct < c.col_tiles; ct += across) {
+    Walk at(c, across, ct);
+    for (; at.tile < c.row_tiles; at.tile += at.tile_step * kAhead) {
+      uint32_t w[kAhead][kWords<TYPE>];
 #pragma unroll
-    for (int i = 0; i < kChunk; i++) {
-      const uint32_t u = __float_as_uint(v[i]) & 0x7FFFFFFF;
-      top = max(top, u < 0x7F800000 ? u : 0);
+      for (int r = 0; r < kAhead; r++)
+        load_chunk<TYPE, ALIGNED>(m, (uint32_t)min((uint64_t)at.row() + (uint64_t)r * at.tile_step * at.per, (uint64_t)m.rows), at.chunk, w[r]);
+#pragma unroll
+      for (int r = 0; r < kAhead; r++) {
+        uint32_t t = top_bits<TYPE>(chunk_top<TYPE>(w[r], 0, kChunk));
+        if (t >= 0x7F800000) {  // without what is not finite
+          t = 0;
+#pragma unroll
+          for (int i = 0; i < kChunk; i++) {
+            const uint32_t u = __float_as_uint(value_of<TYPE>(w[r], i)) & 0x7FFFFFFF;
+            t = max(t, u < 0x7F800000 ? u : 0);
+          }
+        }
+        top = max(top, t);
+      }
     }
   }
   top = block_max(top, smem);
   if (threadIdx.x == 0) partial[blockIdx.x] = top;
 }
 
-// One thread quantises 16 values: half an MXFP4 block (its other half in the lane beside it)
-// or an NVFP4 block, with one load of its values, 8 bytes of codes stored, and the scales of
-// four blocks joined by shuffles into one word of their tile.
-template <int FMT, int TYPE>
-__global__ void __launch_bounds__(kThreads) k_mx_quantize(Matrix m, Cover c, float* global_scale,
-                                                          const uint32_t* partial, uint32_t n_partial, uint8_t* codes,
-                                                          uint8_t* scales, uint64_t row_bytes, uint64_t col_tiles) {
+// One thread quantises 32 values, an MXFP4 block or two NVFP4 blocks: one load of its values,
+// 16 bytes of codes stored, and the scales of four blocks joined by shuffles into one word of
+// their tile.
+template <int FMT, int TYPE, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, FMT == kNvFp4 ? 3 : 4) k_mx_quantize(Matrix m, Cover c, float* global_scale, const uint32_t* partial,
+                                                          uint32_t n_partial, uint8_t* codes, uint8_t* scales,
+                                                          uint64_t row_bytes, uint64_t col_tiles) {
   float g = 1.f, inv6g = 0.f;
   if constexpr (FMT == kNvFp4) {
     if (n_partial) {
@@ -246,48 +348,52 @@ __global__ void __launch_bounds__(kThreads) k_mx_quantize(Matrix m, Cover c, flo
     }
     inv6g = __frcp_rn(6.f * g);
   }
-  for (uint64_t t = blockIdx.x; t < c.tiles; t += gridDim.x) {
-    uint64_t row;
-    uint32_t chunk;
-    place(c, t, row, chunk);
-    float v[kChunk];
-    load_chunk<TYPE>(m, row, chunk, v);
-    uint32_t top = 0;  // as integers, so that a NaN is above every number
-#pragma unroll
-    for (int i = 0; i < kChunk; i++) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFF);
-    uint32_t out[2] = {0, 0}, word;
+  constexpr uint32_t kPer = FMT == kMxFp4 ? 4 : 2;  // chunks of four blocks
+  Walk at(c);
+  const bool writes_codes = (uint64_t)at.chunk * 16 < row_bytes;
+  const bool writes_scales = at.chunk % kPer == 0 && at.chunk / kPer < col_tiles;
+  const uint32_t padded = (m.rows + 127) / 128 * 128;
+  for (; at.tile < c.row_tiles; at.tile += at.tile_step) {
+    const uint32_t row = at.row();
+    uint32_t w[kWords<TYPE>];
+    load_chunk<TYPE, ALIGNED>(m, row, at.chunk, w);
+    uint32_t out[4] = {0, 0, 0, 0}, word;
     if constexpr (FMT == kMxFp4) {
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      const uint32_t top = top_bits<TYPE>(chunk_top<TYPE>(w, 0, 32));
       uint32_t byte = 255;
       if (top < 0x7F800000) {
         // the exponent field less 2: floor(log2(amax)) - 2 + 127, and 0 below the range
         byte = (uint32_t)max((int)(top >> 23) - 2, 0);
         const float inv = __uint_as_float((254 - byte) << 23);  // 2^(127 - byte), a normal number
-        float q[kChunk];
+        float q[32];
 #pragma unroll
-        for (int i = 0; i < kChunk; i++) q[i] = v[i] * inv;  // exact where it matters: above 2^-126
-        out[0] = to_e2m1(q), out[1] = to_e2m1(q + 8);
+        for (int i = 0; i < 32; i++) q[i] = value_of<TYPE>(w, i) * inv;  // exact where it matters: above 2^-126
+#pragma unroll
+        for (int i = 0; i < 4; i++) out[i] = to_e2m1(q + 8 * i);
       }
-      word = byte << (8 * (chunk / 2 % 4));
-      word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
-      word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-    } else {
-      uint32_t byte = 127;
-      if (top < 0x7F800000) {
-        byte = nv_scale(__uint_as_float(top), g, inv6g);
-        nv_codes(v, from_e4m3(byte), g, out);
-      }
-      word = byte << (8 * (chunk % 4));
+      word = byte << (8 * (at.chunk % 4));
       word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
       word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+    } else {
+      word = 0;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const uint32_t top = top_bits<TYPE>(chunk_top<TYPE>(w, 16 * h, 16));
+        uint32_t byte = 127;
+        if (top < 0x7F800000) {
+          byte = nv_scale(__uint_as_float(top), g, inv6g);
+          nv_codes<TYPE>(w, 16 * h, m.base + row * m.stride_bytes + ((uint64_t)at.chunk * kChunk + 16 * h) * mx_value_bytes(TYPE),
+                         from_e4m3(byte), g, out + 2 * h);
+        }
+        word |= byte << (8 * (2 * (at.chunk % 2) + h));
+      }
+      word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
     }
-    if (row < m.rows && (uint64_t)chunk * 8 < row_bytes)
-      *reinterpret_cast<uint2*>(codes + row * row_bytes + (uint64_t)chunk * 8) = make_uint2(out[0], out[1]);
-    constexpr uint32_t kPer = FMT == kMxFp4 ? 8 : 4;  // chunks of four blocks
-    const uint64_t tile = chunk / kPer;
-    if (chunk % kPer == 0 && tile < col_tiles && row < mx_div_up(m.rows, 128) * 128)
-      *reinterpret_cast<uint32_t*>(scales + (row / 128 * col_tiles + tile) * kMxTileBytes +
-                                   mx_in_tile((uint32_t)(row % 128), 0)) = word;
+    if (row < m.rows && writes_codes)
+      *reinterpret_cast<uint4*>(codes + row * row_bytes + (uint64_t)at.chunk * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+    if (row < padded && writes_scales)
+      *reinterpret_cast<uint32_t*>(scales + (row / 128 * col_tiles + at.chunk / kPer) * kMxTileBytes +
+                                   mx_in_tile(row % 128, 0)) = word;
   }
 }
 
@@ -298,116 +404,174 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
   return from_e4m3(b);
 }
 
-// One thread writes one aligned 16-byte vector of the output (8 or 4 values), wherever rows
-// of odd length start: it is the codes, 4 bits each, that are shifted into place. The vector
-// lies in at most two blocks.
+// Values i and i + 1 of eight codes, as floats.
+__device__ __forceinline__ float2 two_values(uint32_t bits, int i) {
+  uint32_t h2;
+  asm("{\n .reg .b8 b, z1, z2, z3;\n mov.b32 {b, z1, z2, z3}, %1;\n cvt.rn.f16x2.e2m1x2 %0, b;\n}\n"
+      : "=r"(h2)
+      : "r"(bits >> (4 * i)));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
+}
+
+// A 16-byte vector of output values.
+template <int TYPE>
+__device__ __forceinline__ uint4 pack_values(const float* v) {
+  uint32_t p[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if constexpr (TYPE == kValFP32) {
+      p[i] = __float_as_uint(v[i]);
+    } else if constexpr (TYPE == kValBF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      p[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      p[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(p[0], p[1], p[2], p[3]);
+}
+
+struct Packed {
+  const uint8_t *codes, *scales;
+  const float* global_scale;
+  uint64_t row_bytes, col_tiles;
+  uint32_t rows, cols;
+};
+
+// Every row of the output starts on a 32-byte boundary: one thread reads back 16 values, 8
+// bytes of codes with one scale, and stores them as 32-byte vectors.
 template <int FMT, int TYPE>
-__global__ void __launch_bounds__(kThreads) k_mx_dequantize(const uint8_t* codes, const uint8_t* scales,
-                                                            const float* global_scale, uint64_t rows, uint32_t cols,
-                                                            uint8_t* out, uint64_t stride_bytes, Cover c,
-                                                            uint64_t row_bytes, uint64_t col_tiles) {
+__global__ void __launch_bounds__(kThreads) k_mx_dequantize(Packed m, uint8_t* out, uint64_t stride_bytes, Cover c) {
+  constexpr int B = (int)mx_value_bytes(TYPE), V = 32 / B;
+  const float g = FMT == kNvFp4 ? *m.global_scale : 1.f;
+  Walk at(c);
+  const uint32_t first = at.chunk * kReadBack;
+  if (first >= m.cols) return;
+  const uint32_t left = m.cols - first, block = first / mx_block(FMT);
+  const uint8_t* st = m.scales + (uint64_t)(block / 4) * kMxTileBytes + block % 4;
+  for (; at.tile < c.row_tiles; at.tile += at.tile_step) {
+    const uint32_t row = at.row();
+    if (row >= m.rows) break;
+    const uint2 bits = __ldg(reinterpret_cast<const uint2*>(m.codes + row * m.row_bytes + (uint64_t)at.chunk * 8));
+    const float s = scale_of<FMT>(__ldg(st + row / 128 * m.col_tiles * kMxTileBytes + mx_in_tile(row % 128, 0)));
+    float v[kReadBack];
+#pragma unroll
+    for (int i = 0; i < kReadBack; i += 2) {
+      const float2 f = two_values(i < 8 ? bits.x : bits.y, i % 8);
+      v[i] = f.x * s, v[i + 1] = f.y * s;
+    }
+    if constexpr (FMT == kNvFp4) {
+#pragma unroll
+      for (int i = 0; i < kReadBack; i++) v[i] *= g;
+    }
+    uint8_t* o = out + row * stride_bytes + (uint64_t)first * B;
+#pragma unroll
+    for (int i = 0; i < kReadBack; i += V) {
+      const uint4 p = pack_values<TYPE>(v + i), r = pack_values<TYPE>(v + i + V / 2);
+      const uint32_t words[8] = {p.x, p.y, p.z, p.w, r.x, r.y, r.z, r.w};
+      if (left >= (uint32_t)i + V) {
+        st_v8(o + i * B, words);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; k++) {
+          if ((uint32_t)(i + k) >= left) continue;
+          if constexpr (B == 4) reinterpret_cast<uint32_t*>(o)[i + k] = words[k];
+          else reinterpret_cast<uint16_t*>(o)[i + k] = (uint16_t)(words[k / 2] >> (16 * (k % 2)));
+        }
+      }
+    }
+  }
+}
+
+// Rows that start anywhere: one thread writes one aligned 16-byte vector of the output (8 or 4
+// values), and it is the codes, 4 bits each, that are shifted into place. The vector lies in at
+// most two blocks.
+template <int FMT, int TYPE>
+__global__ void __launch_bounds__(kThreads) k_mx_dequantize_any(Packed m, uint8_t* out, uint64_t stride_bytes, Cover c) {
   constexpr int B = (int)mx_value_bytes(TYPE), V = 16 / B;
   constexpr uint32_t kBlk = mx_block(FMT);
-  const float g = FMT == kNvFp4 ? *global_scale : 1.f;
-  for (uint64_t t = blockIdx.x; t < c.tiles; t += gridDim.x) {
-    uint64_t row;
-    uint32_t vec;
-    place(c, t, row, vec);
-    if (row >= rows) continue;
+  const float g = FMT == kNvFp4 ? *m.global_scale : 1.f;
+  const int64_t cols = m.cols;
+  Walk at(c);
+  for (; at.tile < c.row_tiles; at.tile += at.tile_step) {
+    const uint32_t row = at.row();
+    if (row >= m.rows) break;
     uint8_t* o = out + row * stride_bytes;
-    const int64_t e0 = (int64_t)vec * V - (int64_t)((reinterpret_cast<uintptr_t>(o) & 15) / B);
-    if (e0 >= (int64_t)cols) continue;
-    const int64_t lo = e0 < 0 ? 0 : e0, hi = e0 + V < (int64_t)cols ? e0 + V : (int64_t)cols;  // values lo .. hi - 1
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(codes + row * row_bytes);
+    const int64_t e0 = (int64_t)at.chunk * V - (int64_t)((reinterpret_cast<uintptr_t>(o) & 15) / B);
+    if (e0 >= cols) continue;
+    const int64_t lo = e0 < 0 ? 0 : e0, hi = e0 + V < cols ? e0 + V : cols;  // values lo .. hi - 1
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(m.codes + row * m.row_bytes);
     const int64_t w0 = e0 >> 3;
     const uint32_t sh = 4 * (uint32_t)(e0 & 7);
     uint32_t bits = w0 >= 0 ? __ldg(w + w0) : 0u;
-    if (sh + 4 * V > 32) bits = __funnelshift_r(bits, (uint64_t)(w0 + 1) * 4 < row_bytes ? __ldg(w + w0 + 1) : 0u, sh);
+    if (sh + 4 * V > 32) bits = __funnelshift_r(bits, (uint64_t)(w0 + 1) * 4 < m.row_bytes ? __ldg(w + w0 + 1) : 0u, sh);
     else bits >>= sh;
     const uint32_t b0 = (uint32_t)lo / kBlk, b1 = (uint32_t)(hi - 1) / kBlk;
-    const uint8_t* st = scales + row / 128 * col_tiles * kMxTileBytes;
-    const uint32_t r = (uint32_t)(row % 128);
-    const float s0 = scale_of<FMT>(__ldg(st + (uint64_t)(b0 / 4) * kMxTileBytes + mx_in_tile(r, b0)));
-    const float s1 = b1 == b0 ? s0 : scale_of<FMT>(__ldg(st + (uint64_t)(b1 / 4) * kMxTileBytes + mx_in_tile(r, b1)));
+    const uint8_t* st = m.scales + row / 128 * m.col_tiles * kMxTileBytes + mx_in_tile(row % 128, 0);
+    const float s0 = scale_of<FMT>(__ldg(st + (uint64_t)(b0 / 4) * kMxTileBytes + b0 % 4));
+    const float s1 = b1 == b0 ? s0 : scale_of<FMT>(__ldg(st + (uint64_t)(b1 / 4) * kMxTileBytes + b1 % 4));
     const int cut = (int)((int64_t)(b0 + 1) * kBlk - e0);  // values from here on are of the second block
     float v[V];
 #pragma unroll
-    for (int i = 0; i < V / 2; i++) {
-      uint32_t h2;
-      asm("{\n .reg .b8 b, z1, z2, z3;\n mov.b32 {b, z1, z2, z3}, %1;\n cvt.rn.f16x2.e2m1x2 %0, b;\n}\n"
-          : "=r"(h2)
-          : "r"(bits >> (8 * i)));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-      v[2 * i] = f.x * (2 * i < cut ? s0 : s1);
-      v[2 * i + 1] = f.y * (2 * i + 1 < cut ? s0 : s1);
+    for (int i = 0; i < V; i += 2) {
+      const float2 f = two_values(bits, i);
+      v[i] = f.x * (i < cut ? s0 : s1);
+      v[i + 1] = f.y * (i + 1 < cut ? s0 : s1);
     }
     if constexpr (FMT == kNvFp4) {
 #pragma unroll
       for (int i = 0; i < V; i++) v[i] *= g;
     }
-    uint32_t p[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if constexpr (TYPE == kValFP32) {
-        p[i] = __float_as_uint(v[i]);
-      } else if constexpr (TYPE == kValBF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        p[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-        p[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    }
-    uint8_t* at = o + e0 * B;
+    const uint4 p = pack_values<TYPE>(v);
+    uint8_t* to = o + e0 * B;
     if (lo == e0 && hi == e0 + V) {
-      *reinterpret_cast<uint4*>(at) = make_uint4(p[0], p[1], p[2], p[3]);
+      *reinterpret_cast<uint4*>(to) = p;
     } else {
+      const uint32_t words[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
       for (int i = 0; i < V; i++) {
         if (e0 + i < lo || e0 + i >= hi) continue;
-        if constexpr (TYPE == kValFP32) reinterpret_cast<uint32_t*>(at)[i] = p[i];
-        else reinterpret_cast<uint16_t*>(at)[i] = (uint16_t)(p[i / 2] >> (16 * (i % 2)));
+        if constexpr (B == 4) reinterpret_cast<uint32_t*>(to)[i] = words[i];
+        else reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(words[i / 2] >> (16 * (i % 2)));
       }
     }
   }
 }
 
-uint32_t grid_of(uint64_t tiles, uint32_t most) { return (uint32_t)(tiles < most ? tiles : most); }
 constexpr uint32_t kGrid = 148 * 8;  // every thread of the device at 256 a block
 
-template <int TYPE>
-cudaError_t launch_quantize(int fmt, const Matrix& m, float* global_scale, bool find, uint8_t* codes, uint8_t* scales,
+template <int FMT, int TYPE, bool ALIGNED>
+cudaError_t launch_quantize(const Matrix& m, float* global_scale, bool find, uint8_t* codes, uint8_t* scales,
                             uint32_t* partial, cudaStream_t st) {
-  const uint64_t col_tiles = mx_col_tiles(fmt, m.cols), chunks = col_tiles * (4 * mx_block(fmt) / kChunk);
+  const uint64_t col_tiles = mx_col_tiles(FMT, m.cols), chunks = col_tiles * (4 * mx_block(FMT) / kChunk);
   uint32_t n_partial = 0;
-  if (fmt == kNvFp4 && find) {
-    const Cover ca = cover(m.rows, mx_div_up(m.cols, kChunk));
-    n_partial = grid_of(ca.tiles, kMaxPartials);
+  if (find) {
+    const Cover ca = cover(m.rows, mx_div_up(m.cols, kChunk), kMaxPartials);
+    n_partial = ca.grid < kMaxPartials ? ca.grid : kMaxPartials;  // one maximum a block
     TimedLaunch t(kIdMxAmax, st);
-    k_mx_amax<TYPE><<<n_partial, kThreads, 0, st>>>(m, ca, partial);
+    k_mx_amax<TYPE, ALIGNED><<<n_partial, kThreads, 0, st>>>(m, ca, partial);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const Cover c = cover(mx_div_up(m.rows, 128) * 128, chunks);
-  const uint64_t rb = mx_row_bytes(m.cols);
+  const Cover c = cover(mx_div_up(m.rows, 128) * 128, chunks, kGrid);
   TimedLaunch t(kIdMxQuantize, st);
-  if (fmt == kMxFp4)
-    k_mx_quantize<kMxFp4, TYPE><<<grid_of(c.tiles, kGrid), kThreads, 0, st>>>(m, c, nullptr, nullptr, 0, codes, scales, rb, col_tiles);
-  else
-    k_mx_quantize<kNvFp4, TYPE><<<grid_of(c.tiles, kGrid), kThreads, 0, st>>>(m, c, global_scale, partial, n_partial, codes, scales, rb, col_tiles);
+  k_mx_quantize<FMT, TYPE, ALIGNED><<<c.grid, kThreads, 0, st>>>(m, c, global_scale, partial, n_partial, codes, scales,
+                                                                  mx_row_bytes(m.cols), col_tiles);
   return cudaGetLastError();
 }
 
 template <int FMT, int TYPE>
-cudaError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, const float* g, uint64_t rows, uint32_t cols,
-                              uint8_t* out, uint64_t stride_bytes, cudaStream_t st) {
-  constexpr uint32_t V = 16 / mx_value_bytes(TYPE);
-  // a row that starts off a 16-byte boundary has one vector more
-  const bool even = reinterpret_cast<uintptr_t>(out) % 16 == 0 && stride_bytes % 16 == 0;
-  const Cover c = cover(rows, even ? mx_div_up(cols, V) : (uint64_t)cols / V + 2);
+cudaError_t launch_dequantize(const Packed& m, uint8_t* out, uint64_t stride_bytes, cudaStream_t st) {
   TimedLaunch t(kIdMxDequantize, st);
-  k_mx_dequantize<FMT, TYPE><<<grid_of(c.tiles, kGrid), kThreads, 0, st>>>(codes, scales, g, rows, cols, out, stride_bytes, c,
-                                                                           mx_row_bytes(cols), mx_col_tiles(FMT, cols));
+  if (reinterpret_cast<uintptr_t>(out) % 32 == 0 && stride_bytes % 32 == 0) {
+    const Cover c = cover(m.rows, mx_div_up(m.cols, kReadBack), kGrid);
+    k_mx_dequantize<FMT, TYPE><<<c.grid, kThreads, 0, st>>>(m, out, stride_bytes, c);
+  } else {
+    // a row that starts off a boundary has a vector more
+    const Cover c = cover(m.rows, (uint64_t)m.cols / (16 / mx_value_bytes(TYPE)) + 2, kGrid);
+    k_mx_dequantize_any<FMT, TYPE><<<c.grid, kThreads, 0, st>>>(m, out, stride_bytes, c);
+  }
   return cudaGetLastError();
 }
 
@@ -442,16 +606,26 @@ zipnn_status zipnn_mx_quantize(zipnn_mx_format format, zipnn_value_type type, co
   if (!device_ok()) return ZIPNN_ERR_UNSUPPORTED;
   Matrix m;
   m.base = static_cast<const uint8_t*>(x);
-  m.rows = rows;
+  m.rows = (uint32_t)rows;
   m.cols = (uint32_t)cols;
   m.stride_bytes = row_stride * B;
   m.end = m.base + (rows - 1) * m.stride_bytes + cols * B;
   uint8_t *c = static_cast<uint8_t*>(codes), *s = static_cast<uint8_t*>(scales);
   uint32_t* p = static_cast<uint32_t*>(ws);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (type == ZIPNN_VALUE_BF16) return cuda_status(launch_quantize<kValBF16>(format, m, global_scale, find, c, s, p, st));
-  if (type == ZIPNN_VALUE_FP32) return cuda_status(launch_quantize<kValFP32>(format, m, global_scale, find, c, s, p, st));
-  return cuda_status(launch_quantize<kValFP16>(format, m, global_scale, find, c, s, p, st));
+  const bool even = reinterpret_cast<uintptr_t>(x) % 32 == 0 && m.stride_bytes % 32 == 0;
+#define ZIPNN_MX_CASE(F, T)                                                                          \
+  if (format == F && type == T)                                                                      \
+    return cuda_status(even ? launch_quantize<F, T, true>(m, global_scale, find, c, s, p, st)       \
+                            : launch_quantize<F, T, false>(m, global_scale, find, c, s, p, st));
+  ZIPNN_MX_CASE(kMxFp4, kValBF16)
+  ZIPNN_MX_CASE(kMxFp4, kValFP32)
+  ZIPNN_MX_CASE(kMxFp4, kValFP16)
+  ZIPNN_MX_CASE(kNvFp4, kValBF16)
+  ZIPNN_MX_CASE(kNvFp4, kValFP32)
+  ZIPNN_MX_CASE(kNvFp4, kValFP16)
+#undef ZIPNN_MX_CASE
+  return ZIPNN_ERR_INVALID_ARG;
 }
 
 zipnn_status zipnn_mx_dequantize(zipnn_mx_format format, zipnn_value_type type, const void* codes, const void* scales,
@@ -463,12 +637,12 @@ zipnn_status zipnn_mx_dequantize(zipnn_mx_format format, zipnn_value_type type, 
   if (reinterpret_cast<uintptr_t>(out) % B || row_stride < cols || row_stride > kMxMaxCols) return ZIPNN_ERR_INVALID_ARG;
   if (format == ZIPNN_NVFP4 && (!global_scale || reinterpret_cast<uintptr_t>(global_scale) % 4)) return ZIPNN_ERR_INVALID_ARG;
   if (!device_ok()) return ZIPNN_ERR_UNSUPPORTED;
-  const uint8_t *c = static_cast<const uint8_t*>(codes), *s = static_cast<const uint8_t*>(scales);
+  const Packed m{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), global_scale, mx_row_bytes(cols),
+                 mx_col_tiles(format, cols), (uint32_t)rows, (uint32_t)cols};
   uint8_t* o = static_cast<uint8_t*>(out);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const uint32_t n = (uint32_t)cols;
 #define ZIPNN_MX_CASE(F, T) \
-  if (format == F && type == T) return cuda_status(launch_dequantize<F, T>(c, s, global_scale, rows, n, o, row_stride * B, st));
+  if (format == F && type == T) return cuda_status(launch_dequantize<F, T>(m, o, row_stride * B, st));
   ZIPNN_MX_CASE(kMxFp4, kValBF16)
   ZIPNN_MX_CASE(kMxFp4, kValFP32)
   ZIPNN_MX_CASE(kMxFp4, kValFP16)
