@@ -34,19 +34,37 @@ def _format(format):
     return f if f is not None else _fail(f"mx: format {format!r} is not one of {sorted(_FORMATS)}")
 
 
+# the handle of a device's current stream; the public way to it builds a Stream object, which
+# takes longer (3.2 us) than the whole call of a small operator
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _call(fn, what, device, *args):
     """fn(*args, stream) on the current stream of the tensors' device, made current."""
-    if device.index == torch.cuda.current_device():
-        Z.check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+    i = device.index
+    if i == torch.cuda.current_device():
+        status = fn(*args, _current_stream(i))
     else:
         with torch.cuda.device(device):
-            Z.check(fn(*args, torch.cuda.current_stream().cuda_stream), what)
+            status = fn(*args, _current_stream(i))
+    if status:
+        Z.check(status, what)
 
 
 def _use(stream, device):
     """`stream` (a torch stream or a raw handle on `device`) as the current one: what a call
     allocates then belongs to the stream that writes it."""
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+
+
+def _row_bytes(cols):
+    return (cols + 31) // 32 * 16  # zipnn_mx_row_bytes
+
+
+def _scale_bytes(format, rows, cols):
+    per = 4 * BLOCK[format]
+    return (rows + 127) // 128 * ((cols + per - 1) // per) * 512  # zipnn_mx_scale_bytes
 
 
 def _rows(shape):
@@ -74,11 +92,13 @@ class MxTensor:
             _fail("MxTensor: at least one dimension, the last not empty")
         self.cols = self.shape[-1]
         self.rows = self.shape[0] if len(self.shape) == 2 else _rows(self.shape)
+        if self.rows > 1 << 31 or self.cols > 1 << 31:
+            _fail("MxTensor: at most 2^31 rows and columns")
         if not (codes.is_cuda and codes.is_contiguous() and codes.element_size() == 1 and
-                codes.numel() == self.rows * Z.zipnn_mx_row_bytes(self.cols)):
+                codes.numel() == self.rows * _row_bytes(self.cols)):
             _fail("MxTensor: codes are rows x zipnn_mx_row_bytes(cols) contiguous CUDA bytes")
         if not (scales.device == codes.device and scales.is_contiguous() and scales.element_size() == 1 and
-                scales.numel() == (Z.zipnn_mx_scale_bytes(f, self.rows, self.cols) if self.rows else 0)):
+                scales.numel() == _scale_bytes(format, self.rows, self.cols)):
             _fail("MxTensor: scales are zipnn_mx_scale_bytes contiguous bytes beside the codes")
         if f == Z.NVFP4:
             g = global_scale
@@ -86,6 +106,13 @@ class MxTensor:
                 _fail("MxTensor: nvfp4 has a global_scale, one FP32 value on the codes' device")
         elif global_scale is not None:
             _fail("MxTensor: mxfp4 has no global_scale")
+
+    @classmethod
+    def _of(cls, codes, scales, shape, rows, cols, format, global_scale):
+        """What a call of this module made, which needs no checks."""
+        q = object.__new__(cls)
+        q.codes, q.scales, q.shape, q.rows, q.cols, q.format, q.global_scale = codes, scales, shape, rows, cols, format, global_scale
+        return q
 
     @property
     def device(self):
@@ -119,46 +146,41 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
     if stream is not None:
         with _use(stream, x.device):
             return quantize(x, format, global_scale)
-    f = _format(format)
-    if x.dtype not in _VALUES or not x.is_cuda or x.dim() == 0 or x.shape[-1] == 0:
+    f, type = _format(format), _VALUES.get(x.dtype)
+    if type is None or not x.is_cuda or x.dim() == 0 or x.shape[-1] == 0:
         _fail("mx.quantize: a CUDA tensor (..., K) of BF16, FP16 or FP32")
     shape, dev = tuple(x.shape), x.device
     cols = shape[-1]
-    m = x if x.dim() == 2 else x.reshape(-1, cols)
+    m = x if len(shape) == 2 else x.reshape(-1, cols)
     rows = m.shape[0]
-    if (cols > 1 and m.stride(1) != 1) or (rows > 1 and m.stride(0) < cols):
-        m = m.contiguous()
+    stride = m.stride(0) if rows > 1 else cols
+    if (cols > 1 and m.stride(1) != 1) or stride < cols:
+        m, stride = m.contiguous(), cols
+    find = False
     if f == Z.NVFP4:
         find = global_scale is None
         if find:
             global_scale = torch.empty(1, dtype=torch.float32, device=dev)
         elif global_scale.dtype != torch.float32 or global_scale.numel() != 1 or global_scale.device != dev:
             _fail("mx.quantize: global_scale is one FP32 value on x's device")
-    else:
-        find = False
-        if global_scale is not None:
-            _fail("mx.quantize: mxfp4 has no global_scale")
-    if rows == 0:
-        if find:
-            global_scale.fill_(1.0)
-        return MxTensor(torch.empty((0,), dtype=torch.uint8, device=dev),
-                        torch.empty((0,), dtype=_SCALE_DTYPES[format], device=dev), shape, format, global_scale)
-    rb, sb = Z.zipnn_mx_row_bytes(cols), Z.zipnn_mx_scale_bytes(f, rows, cols)
-    if sb == 0:
+    elif global_scale is not None:
+        _fail("mx.quantize: mxfp4 has no global_scale")
+    if rows > 1 << 31 or cols > 1 << 31:
         _fail("mx.quantize: at most 2^31 rows and columns")
-    codes = torch.empty((rows, rb), dtype=torch.float4_e2m1fn_x2, device=dev)
-    scales = torch.empty((sb,), dtype=_SCALE_DTYPES[format], device=dev)
-    ws = torch.empty((Z.MX_WORKSPACE_BYTES,), dtype=torch.uint8, device=dev) if find else None
-    _call(Z.zipnn_mx_quantize, "zipnn_mx_quantize", dev, f, _VALUES[x.dtype], m.data_ptr(), rows, cols,
-          m.stride(0) if rows > 1 else cols, None if global_scale is None else global_scale.data_ptr(), int(find),
-          codes.data_ptr(), scales.data_ptr(), ws.data_ptr() if find else None, Z.MX_WORKSPACE_BYTES if find else 0)
-    return MxTensor(codes, scales, shape, format, global_scale)
+    codes = torch.empty((rows, _row_bytes(cols)), dtype=torch.float4_e2m1fn_x2, device=dev)
+    scales = torch.empty(_scale_bytes(format, rows, cols), dtype=_SCALE_DTYPES[format], device=dev)
+    if rows:
+        ws = torch.empty(Z.MX_WORKSPACE_BYTES, dtype=torch.uint8, device=dev) if find else None
+        _call(Z.zipnn_mx_quantize, "zipnn_mx_quantize", dev, f, type, m.data_ptr(), rows, cols, stride,
+              None if global_scale is None else global_scale.data_ptr(), find, codes.data_ptr(), scales.data_ptr(),
+              None if ws is None else ws.data_ptr(), Z.MX_WORKSPACE_BYTES)
+    elif find:
+        global_scale.fill_(1.0)
+    return MxTensor._of(codes, scales, shape, rows, cols, format, global_scale)
 
 
 def _out(out, shape, dtype, device, what):
-    """A new tensor, or the caller's where it can be written: its last dimension contiguous."""
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+    """The caller's tensor where it can be written: its last dimension contiguous."""
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
         _fail(f"{what}: out is a {dtype} tensor {tuple(shape)} on {device}")
     if not (out.is_contiguous() or (out.dim() == 2 and (out.shape[1] == 1 or out.stride(1) == 1) and out.stride(0) >= out.shape[1])):
@@ -171,13 +193,18 @@ def dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
     if stream is not None:
         with _use(stream, q.device):
             return dequantize(q, dtype, out)
-    if dtype not in _VALUES:
+    type = _VALUES.get(dtype)
+    if type is None:
         _fail("mx.dequantize: to BF16, FP16 or FP32")
-    out = _out(out, q.shape, dtype, q.device, "mx.dequantize")
+    dev, stride = q.codes.device, q.cols
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=dev)
+    else:
+        _out(out, q.shape, dtype, dev, "mx.dequantize")
+        stride = out.stride(0) if out.dim() == 2 and q.rows > 1 else stride
     if q.rows:
-        stride = out.stride(0) if out.dim() == 2 and q.rows > 1 else q.cols
-        _call(Z.zipnn_mx_dequantize, "zipnn_mx_dequantize", q.device, _FORMATS[q.format], _VALUES[dtype],
-              q.codes.data_ptr(), q.scales.data_ptr(), q._global, q.rows, q.cols, out.data_ptr(), stride)
+        _call(Z.zipnn_mx_dequantize, "zipnn_mx_dequantize", dev, _FORMATS[q.format], type, q.codes.data_ptr(),
+              q.scales.data_ptr(), q._global, q.rows, q.cols, out.data_ptr(), stride)
     return out
 
 
@@ -192,14 +219,19 @@ def matmul(a, b, dtype=torch.bfloat16, out=None, stream=None):
         _fail("mx.matmul: b is an MxTensor")
     if not isinstance(a, MxTensor):
         a = quantize(a, b.format)
-    if a.format != b.format or a.cols != b.cols or len(b.shape) != 2 or a.device != b.device or dtype not in _VALUES:
+    dev, type = a.codes.device, _VALUES.get(dtype)
+    if a.format != b.format or a.cols != b.cols or len(b.shape) != 2 or b.codes.device != dev or type is None:
         _fail("mx.matmul: a (..., K) and b (N, K) of one format, on one device, to BF16, FP16 or FP32")
-    out = _out(out, a.shape[:-1] + (b.rows,), dtype, a.device, "mx.matmul")
+    shape, stride = a.shape[:-1] + (b.rows,), b.rows
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _out(out, shape, dtype, dev, "mx.matmul")
+        stride = out.stride(0) if out.dim() == 2 and a.rows > 1 else stride
     if a.rows and b.rows:
-        stride = out.stride(0) if out.dim() == 2 and a.rows > 1 else b.rows
-        _call(Z.zipnn_mx_matmul, "zipnn_mx_matmul", a.device, _FORMATS[a.format], a.codes.data_ptr(), a.scales.data_ptr(),
-              a._global, b.codes.data_ptr(), b.scales.data_ptr(), b._global, a.rows, b.rows, a.cols, _VALUES[dtype],
-              out.data_ptr(), stride)
+        _call(Z.zipnn_mx_matmul, "zipnn_mx_matmul", dev, _FORMATS[a.format], a.codes.data_ptr(), a.scales.data_ptr(),
+              a._global, b.codes.data_ptr(), b.scales.data_ptr(), b._global, a.rows, b.rows, a.cols, type, out.data_ptr(),
+              stride)
     return out
 
 

@@ -36,15 +36,19 @@ def _pool_desc(t, what):
     """(descriptor, bytes of a page) of a (planes, pages, ...) CUDA tensor with contiguous pages."""
     if not t.is_cuda or t.dim() < 3:
         _fail(f"{what}: a CUDA tensor (planes, pages, ...)")
-    size, n = t.element_size(), 1
-    for d in range(t.dim() - 1, 1, -1):
-        if t.shape[d] != 1 and t.stride(d) != n:
-            _fail(f"{what}: pages are contiguous")
-        n *= t.shape[d]
+    shape, size = t.shape, t.element_size()
+    n = 1
+    if t.is_contiguous():
+        n = t.numel() // max(1, shape[0] * shape[1])
+    else:
+        for d in range(t.dim() - 1, 1, -1):
+            if shape[d] != 1 and t.stride(d) != n:
+                _fail(f"{what}: pages are contiguous")
+            n *= shape[d]
     # the stride of a dimension of one element says nothing
-    page = t.stride(1) * size if t.shape[1] > 1 else n * size
-    plane = t.stride(0) * size if t.shape[0] > 1 else page * t.shape[1]
-    return Z.PagePoolDesc(t.data_ptr(), plane, page, t.shape[0], t.shape[1]), n * size
+    page = t.stride(1) * size if shape[1] > 1 else n * size
+    plane = t.stride(0) * size if shape[0] > 1 else page * shape[1]
+    return Z.PagePoolDesc(t.data_ptr(), plane, page, shape[0], shape[1]), n * size
 
 
 def _ids(v, device, what):
@@ -72,8 +76,9 @@ def copy(src, src_ids, dst, dst_ids, count=None, ws=None, stream=None):
         src_ids = _ids(src_ids, dst.device, "pages.copy: src_ids")
     if dst_ids is not None:
         dst_ids = _ids(dst_ids, dst.device, "pages.copy: dst_ids")
-    n = min(v.numel() for v in (src_ids, dst_ids) if v is not None) if (src_ids is not None or dst_ids is not None) else min(a.pages, b.pages)
-    if src_ids is not None and dst_ids is not None and src_ids.numel() != dst_ids.numel():
+    lists = [v.numel() for v in (src_ids, dst_ids) if v is not None]
+    n = min(lists) if lists else min(a.pages, b.pages)
+    if n != max(lists, default=n):
         _fail("pages.copy: as many destinations as sources")
     if count is not None:
         if not 0 <= count <= n:
@@ -128,6 +133,8 @@ class PagePool:
         self._table = Z.PageTableDesc(self.refs.data_ptr(), self.lens.data_ptr(), self.tables.data_ptr(), max_seqs, slots,
                                       page_tokens)
         self.ws = torch.zeros(Z.zipnn_pages_workspace_bytes(max_seqs, P), dtype=torch.uint8, device=pages.device)
+        self._pool_ref, self._table_ref = ctypes.byref(self._pool), ctypes.byref(self._table)
+        self._ws_ptr, self._ws_bytes = self.ws.data_ptr(), self.ws.numel()
         self.live = self.ws[4:8].view(torch.int32)  # pages in use, as the last `compact` counted them
 
     def fork(self, rows, parents, lens, stream=None):
@@ -140,9 +147,8 @@ class PagePool:
         n = rows.numel()
         if parents.numel() != n or lens.numel() != n or n > self._table.seqs:
             _fail("PagePool.fork: a parent and a length for each row, each row at most once")
-        _call(Z.zipnn_pages_fork, "zipnn_pages_fork", self.device, ctypes.byref(self._pool), self.page_bytes,
-              ctypes.byref(self._table), rows.data_ptr(), parents.data_ptr(), lens.data_ptr(), n, self.ws.data_ptr(),
-              self.ws.numel())
+        _call(Z.zipnn_pages_fork, "zipnn_pages_fork", self.device, self._pool_ref, self.page_bytes, self._table_ref, rows.data_ptr(),
+              parents.data_ptr(), lens.data_ptr(), n, self._ws_ptr, self._ws_bytes)
 
     def free(self, rows, compact=False, stream=None):
         """The sequences in `rows` give their pages back; with compact, the gaps are closed
@@ -151,8 +157,8 @@ class PagePool:
             with _use(stream, self.device):
                 return self.free(rows, compact)
         rows = _ids(rows, self.device, "PagePool.free")
-        _call(Z.zipnn_pages_free, "zipnn_pages_free", self.device, ctypes.byref(self._pool), self.page_bytes,
-              ctypes.byref(self._table), rows.data_ptr(), rows.numel(), int(compact), self.ws.data_ptr(), self.ws.numel())
+        _call(Z.zipnn_pages_free, "zipnn_pages_free", self.device, self._pool_ref, self.page_bytes, self._table_ref,
+              rows.data_ptr(), rows.numel(), compact, self._ws_ptr, self._ws_bytes)
 
     def compact(self, stream=None):
         """Close the gaps: afterwards the pages in use are the first `live` ones."""
