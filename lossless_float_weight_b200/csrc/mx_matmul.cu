@@ -39,7 +39,7 @@ struct Args {
   uint32_t col_tiles;          // scale tiles along a row
   uint32_t stages, mmas;       // of the whole row
   uint32_t split;              // blocks of a cluster, each a range of the stages
-  int type, p_is_n;
+  int type, p_is_n, pairs;
 };
 
 template <int FMT, int BN>
@@ -78,6 +78,25 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t addr) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc_scales(addr)) : "memory");
 }
+
+// One lane of a warp that is converged here. The loops around the instructions for the tensor
+// cores and TMA are run by the whole warp, and only the instructions themselves by this lane:
+// their operands live in uniform registers, which a branch on the lane number around the loops
+// would put out of reach (a 4096 x 11008 x 4096 product took 118 us so, moving each operand there).
+__device__ __forceinline__ bool elect() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// A ring of stages: the place of the next one, and how often the ring was gone round (mod 2).
+struct Ring {
+  uint32_t at = 0, parity = 0;
+  __device__ __forceinline__ void next(uint32_t depth) {
+    if (++at == depth) at = 0, parity ^= 1;
+  }
+};
 
 // Which two of a column's four scale bytes an MXFP4 instruction takes is part of its
 // descriptor; an NVFP4 instruction takes all four.
@@ -153,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
   volatile uint32_t* failed = tmem_at + 1;
 
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
   const uint32_t tile = blockIdx.x / a.split, rank = blockIdx.x % a.split;
   const uint32_t p0 = tile / a.q_tiles * 128, q0 = tile % a.q_tiles * BN;
   const uint32_t lo = (uint32_t)((uint64_t)a.stages * rank / a.split), hi = (uint32_t)((uint64_t)a.stages * (rank + 1) / a.split);
@@ -173,57 +192,64 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_at);
+  const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(tmem_at));
 
   if (warp == 4) {
-    if (lane == 0) {
-      for (uint32_t i = lo; i < hi; i++) {
-        const uint32_t n = i - lo, s = n % S::kDepth;
-        if (n >= S::kDepth && !mbar_wait_bounded(empty + s, (n / S::kDepth - 1) & 1, kWaitPolls)) {
-          *failed = 1;
-          break;
-        }
-        uint8_t* st = smem + s * S::kStage;
-        const uint32_t t0 = i * S::kTiles, bytes = min(S::kTiles, a.col_tiles - t0) * kMxTileBytes;
-        const uint32_t halves = S::kHalves == 2 && q0 + 128 < a.q_rows ? 2 : 1;
-        mbar_expect_tx(full + s, S::kP + S::kQ + bytes * (1 + halves));
-        tma_2d(st, &p_map, (int32_t)(i * kStageBytesK), (int32_t)p0, full + s);
-        tma_2d(st + S::kP, &q_map, (int32_t)(i * kStageBytesK), (int32_t)q0, full + s);
-        uint8_t* sc = st + S::kP + S::kQ;
-        bulk_g2s(sc, a.p_scales + ((uint64_t)(p0 / 128) * a.col_tiles + t0) * kMxTileBytes, bytes, full + s);
-        for (uint32_t h = 0; h < halves; h++)
-          bulk_g2s(sc + S::kSp + h * S::kSp, a.q_scales + ((uint64_t)(q0 / 128 + h) * a.col_tiles + t0) * kMxTileBytes, bytes, full + s);
+    const bool one = elect();
+    const uint32_t halves = S::kHalves == 2 && q0 + 128 < a.q_rows ? 2 : 1;
+    Ring r;
+    for (uint32_t i = lo; i < hi; i++, r.next(S::kDepth)) {
+      if (i - lo >= S::kDepth && !mbar_wait_bounded(empty + r.at, r.parity ^ 1, kWaitPolls)) {
+        *failed = 1;
+        break;
       }
+      if (one) {
+        uint8_t* st = smem + r.at * S::kStage;
+        uint64_t* bar = full + r.at;
+        const uint32_t t0 = i * S::kTiles, bytes = min(S::kTiles, a.col_tiles - t0) * kMxTileBytes;
+        mbar_expect_tx(bar, S::kP + S::kQ + bytes * (1 + halves));
+        tma_2d(st, &p_map, (int32_t)(i * kStageBytesK), (int32_t)p0, bar);
+        tma_2d(st + S::kP, &q_map, (int32_t)(i * kStageBytesK), (int32_t)q0, bar);
+        uint8_t* sc = st + S::kP + S::kQ;
+        bulk_g2s(sc, a.p_scales + ((uint64_t)(p0 / 128) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
+        for (uint32_t h = 0; h < halves; h++)
+          bulk_g2s(sc + S::kSp + h * S::kSp, a.q_scales + ((uint64_t)(q0 / 128 + h) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp == 5) {
-    if (lane == 0) {
-      for (uint32_t i = lo; i < hi; i++) {
-        const uint32_t n = i - lo, s = n % S::kDepth;
-        if (!mbar_wait_bounded(full + s, (n / S::kDepth) & 1, kWaitPolls)) {
-          *failed = 1;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t st = smem_addr(smem + s * S::kStage), sc = st + S::kP + S::kQ;
-        const uint32_t tp = tmem + BN + s * S::kScaleCols, tq = tp + 4 * S::kTiles;
-        const uint32_t tiles = min(S::kTiles, a.col_tiles - i * S::kTiles);
-        for (uint32_t t = 0; t < tiles; t++) {
+    const bool one = elect();
+    Ring r;
+    uint32_t left = a.mmas - lo * (kStageK / kMmaK);  // instructions to the end of the row
+    for (uint32_t i = lo; i < hi; i++, r.next(S::kDepth), left -= kStageK / kMmaK) {
+      if (!mbar_wait_bounded(full + r.at, r.parity, kWaitPolls)) {
+        *failed = 1;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t st = smem_addr(smem) + r.at * S::kStage, sc = st + S::kP + S::kQ;
+      const uint32_t tp = tmem + BN + r.at * S::kScaleCols, tq = tp + 4 * S::kTiles;
+      if (one) {
+        // scale tiles that the row does not have are copied too: nothing reads them
+#pragma unroll
+        for (uint32_t t = 0; t < S::kTiles; t++) {
           copy_scales(tp + 4 * t, sc + t * kMxTileBytes);
+#pragma unroll
           for (uint32_t h = 0; h < S::kHalves; h++)
             copy_scales(tq + 4 * (t * S::kHalves + h), sc + S::kSp + h * S::kSp + t * kMxTileBytes);
         }
 #pragma unroll
         for (uint32_t k = 0; k < kStageK / kMmaK; k++) {
-          if (i * (kStageK / kMmaK) + k >= a.mmas) break;
+          if (k >= left) break;
           const uint32_t t = FMT == kMxFp4 ? k / 2 : k, id = FMT == kMxFp4 ? k % 2 * 2 : 0;
           mma<FMT>(tmem, desc_codes(st + k * 32), desc_codes(st + S::kP + k * 32), instr<FMT, BN>(id), tp + 4 * t,
-                   tq + 4 * t * S::kHalves, n + k > 0);
+                   tq + 4 * t * S::kHalves, i + k > lo);
         }
-        commit(empty + s);
+        commit(empty + r.at);
       }
-      commit(done);
+      __syncwarp();
     }
+    if (one) commit(done);
     __syncwarp();
   } else {
     if (!mbar_wait_bounded(done, 0, kWaitPolls)) *failed = 1;
@@ -272,6 +298,247 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   if (warp == 5) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols));
+  }
+}
+
+// ---- Two blocks to a tile --------------------------------------------------------------
+// Large products are bound by what the codes' tiles cost between L2 and shared memory: a stage
+// of a 128 x 128 tile brings 34 KB for 256 cycles of the tensor cores. Here the two blocks of a
+// cluster compute 256 x BN together (cta_group::2): each brings its own 128 rows of P and half
+// of the rows of Q, and both read both halves. One thread of the first block issues the
+// instructions for both, and the sums of a tile leave tensor memory through the registers of
+// eight warps, whose stores overlap with the next tile's instructions. Blocks walk over the
+// tiles, one pair on two SMs.
+constexpr int kPairThreads = 320;
+
+template <int FMT, int BN>
+struct PairShape {
+  static constexpr uint32_t kTiles = kStageK / (4 * mx_block(FMT));
+  static constexpr uint32_t kHalves = BN / 128;  // row tiles of Q's scales: every block needs all of them
+  static constexpr uint32_t kP = 128 * kStageBytesK, kQ = BN / 2 * kStageBytesK;
+  static constexpr uint32_t kSp = kTiles * kMxTileBytes, kSq = kSp * kHalves;
+  static constexpr uint32_t kBytes = kP + kQ + kSp + kSq;
+  static constexpr uint32_t kStage = (kBytes + 1023) / 1024 * 1024;
+  static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kHalves);
+  static constexpr uint32_t kFit = (227 * 1024 - 1024 - 512) / kStage, kRoom = (512 - BN) / kScaleCols;
+  static constexpr uint32_t kDepth = kFit < kRoom ? kFit : kRoom;
+  static constexpr uint32_t kSmem = kDepth * kStage + 1024 + 512;
+};
+
+__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+               "l"(map), "r"(x), "r"(y), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+               "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void pair_copy_scales(uint32_t taddr, uint32_t addr) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc_scales(addr)) : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
+  if constexpr (FMT == kMxFp4) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+        : "memory");
+  }
+}
+// Arrives at the barrier of both blocks when the instructions issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void load_sums32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+template <typename T>
+__device__ __forceinline__ T to_value(float v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else return T(v);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_column(T* out, uint64_t ldo, uint32_t n, const float* v) {
+  if (n >= (uint32_t)N) {
+#pragma unroll
+    for (int c = 0; c < N; c++) out[c * ldo] = to_value<T>(v[c]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c++)
+      if ((uint32_t)c < n) out[c * ldo] = to_value<T>(v[c]);
+  }
+}
+
+struct PairMaps {
+  CUtensorMap p, q, sp, sq;
+};
+
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid_constant__ PairMaps maps, const Args a) {
+  using S = PairShape<FMT, BN>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kDepth * S::kStage);
+  uint64_t *empty = full + S::kDepth, *sums_full = empty + S::kDepth, *sums_empty = sums_full + 1;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sums_empty + 1);
+  volatile uint32_t* failed = tmem_at + 1;
+
+  const uint32_t warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, rank = blockIdx.x & 1;
+  const uint32_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const uint32_t tiles = (a.p_rows + 255) / 256 * a.q_tiles;
+
+  if (warp == 8 && lane == 0) {
+    for (uint32_t i = 0; i < S::kDepth; i++) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    mbar_init(sums_full, 1);
+    mbar_init(sums_empty, 16);  // eight warps of two blocks
+    *failed = 0;
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_at)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(tmem_at));
+
+  if (warp == 8) {
+    const bool one = elect();
+    Ring r;
+    uint32_t n = 0;  // stages brought so far
+    for (uint32_t t = pair; t < tiles && !*failed; t += pairs) {
+      const uint32_t p0 = t / a.q_tiles * 256 + rank * 128, q0 = t % a.q_tiles * BN;
+      for (uint32_t i = 0; i < a.stages; i++, n++, r.next(S::kDepth)) {
+        if (n >= S::kDepth && !mbar_wait_bounded(empty + r.at, r.parity ^ 1, kWaitPolls)) {
+          *failed = 1;
+          break;
+        }
+        if (one) {
+          // both blocks' bytes count at the first one's barrier
+          if (rank == 0) mbar_expect_tx(full + r.at, 2 * S::kBytes);
+          const uint32_t st = smem_addr(smem) + r.at * S::kStage, bar = peer(smem_addr(full + r.at), 0);
+          tma_pair_2d(st, &maps.p, (int32_t)(i * kStageBytesK), (int32_t)p0, bar);
+          tma_pair_2d(st + S::kP, &maps.q, (int32_t)(i * kStageBytesK), (int32_t)(q0 + rank * (BN / 2)), bar);
+          tma_pair_3d(st + S::kP + S::kQ, &maps.sp, 0, (int32_t)(i * S::kTiles), (int32_t)(p0 / 128), bar);
+          tma_pair_3d(st + S::kP + S::kQ + S::kSp, &maps.sq, 0, (int32_t)(i * S::kTiles), (int32_t)(q0 / 128), bar);
+        }
+        __syncwarp();
+      }
+    }
+    // the last arrivals at this block's barriers, which the other block's thread sends
+    for (uint32_t k = 0; k < S::kDepth && !*failed; k++, n++, r.next(S::kDepth))
+      if (n >= S::kDepth && !mbar_wait_bounded(empty + r.at, r.parity ^ 1, kWaitPolls)) *failed = 1;
+  } else if (warp == 9 && rank == 0) {
+    const bool one = elect();
+    Ring r;
+    uint32_t turn = 0;  // parity of the tiles that the sums have left
+    for (uint32_t t = pair; t < tiles && !*failed; t += pairs, turn ^= 1) {
+      if (t != pair && !mbar_wait_bounded(sums_empty, turn ^ 1, kWaitPolls)) {
+        *failed = 1;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      uint32_t left = a.mmas;
+      for (uint32_t i = 0; i < a.stages; i++, r.next(S::kDepth), left -= kStageK / kMmaK) {
+        if (!mbar_wait_bounded(full + r.at, r.parity, kWaitPolls)) {
+          *failed = 1;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t st = smem_addr(smem) + r.at * S::kStage, sc = st + S::kP + S::kQ;
+        const uint32_t tp = tmem + BN + r.at * S::kScaleCols, tq = tp + 4 * S::kTiles;
+        if (one) {
+#pragma unroll
+          for (uint32_t j = 0; j < S::kTiles; j++) {
+            pair_copy_scales(tp + 4 * j, sc + j * kMxTileBytes);
+#pragma unroll
+            for (uint32_t h = 0; h < S::kHalves; h++)
+              pair_copy_scales(tq + 4 * (j * S::kHalves + h), sc + S::kSp + h * S::kSp + j * kMxTileBytes);
+          }
+#pragma unroll
+          for (uint32_t k = 0; k < kStageK / kMmaK; k++) {
+            if (k >= left) break;
+            const uint32_t j = FMT == kMxFp4 ? k / 2 : k, id = FMT == kMxFp4 ? k % 2 * 2 : 0;
+            // 256 rows: twice the 128 of one block
+            pair_mma<FMT>(tmem, desc_codes(st + k * 32), desc_codes(st + S::kP + k * 32), instr<FMT, BN>(id) + (1u << 27), tp + 4 * j,
+                          tq + 4 * j * S::kHalves, i + k > 0);
+          }
+          pair_commit(empty + r.at);
+        }
+        __syncwarp();
+      }
+      if (one) pair_commit(sums_full);
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    const float g = FMT == kNvFp4 ? *a.ga : 1.f, g1 = FMT == kNvFp4 ? *a.gb : 1.f;
+    const uint32_t quarter = warp % 4, half = warp / 4, leader_bar = peer(smem_addr(sums_empty), 0);
+    constexpr int kCols = BN / 2;  // of one warp
+    uint32_t k_tile = 0;
+    for (uint32_t t = pair; t < tiles; t += pairs, k_tile++) {
+      const uint32_t p = t / a.q_tiles * 256 + rank * 128 + quarter * 32 + lane, q = t % a.q_tiles * BN + half * kCols;
+      if (!mbar_wait_bounded(sums_full, k_tile & 1, kWaitPolls)) {
+        *failed = 1;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      float v[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32) load_sums32(tmem + (quarter * 32 << 16) + half * kCols + c, v + c);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive_at(leader_bar);
+      if (p < a.p_rows && q < a.q_rows && !*failed) {
+        const uint32_t cols = a.q_rows - q;
+        if constexpr (FMT == kNvFp4) {
+#pragma unroll
+          for (int c = 0; c < kCols; c++) v[c] = v[c] * g * g1;
+        }
+        const uint64_t at = (uint64_t)q * a.ldo + p;
+        if (a.type == kValFP32) store_column<float, kCols>(reinterpret_cast<float*>(a.out) + at, a.ldo, cols, v);
+        else if (a.type == kValBF16) store_column<__nv_bfloat16, kCols>(reinterpret_cast<__nv_bfloat16*>(a.out) + at, a.ldo, cols, v);
+        else store_column<__half, kCols>(reinterpret_cast<__half*>(a.out) + at, a.ldo, cols, v);
+      }
+    }
+    __syncwarp();
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();  // neither block's barriers and tensor memory go while the other still uses them
+  if (*failed && threadIdx.x == 0) atomicMax(&g_mx_status, kStTimeout);
+  if (warp == 9) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
 }
 
@@ -345,8 +612,55 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, uint64_t cols, Args
   return cudaLaunchKernelEx(&cfg, k_mx_matmul<FMT, BN>, pm, qm, a);
 }
 
+// Scale tiles as (row tiles, tiles along a row, 128 words of 4 bytes); zeros outside.
+bool scale_map(CUtensorMap* m, const uint8_t* scales, uint64_t row_tiles, uint64_t col_tiles, uint32_t box_tiles, uint32_t box_rows) {
+  EncodeTiled f = encode_tiled();
+  const cuuint64_t dims[3] = {kMxTileBytes / 4, col_tiles, row_tiles}, strides[2] = {kMxTileBytes, kMxTileBytes * col_tiles};
+  const cuuint32_t boxes[3] = {kMxTileBytes / 4, box_tiles, box_rows}, steps[3] = {1, 1, 1};
+  return f && f(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(scales), dims, strides, boxes, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, int BN>
+cudaError_t launch_pairs(const Operand& p, const Operand& q, uint64_t cols, Args a, cudaStream_t st) {
+  using S = PairShape<FMT, BN>;
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(k_mx_matmul_pair<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  PairMaps maps;
+  const uint64_t rb = mx_row_bytes(cols);
+  if (!code_map(&maps.p, p.codes, p.rows, rb, 128) || !code_map(&maps.q, q.codes, q.rows, rb, BN / 2) ||
+      !scale_map(&maps.sp, p.scales, mx_div_up(p.rows, 128), a.col_tiles, S::kTiles, 1) ||
+      !scale_map(&maps.sq, q.scales, mx_div_up(q.rows, 128), a.col_tiles, S::kTiles, S::kHalves))
+    return cudaErrorUnknown;
+  a.q_tiles = (uint32_t)mx_div_up(q.rows, BN);
+  const uint64_t tiles = mx_div_up(p.rows, 256) * a.q_tiles, most = (uint64_t)sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((uint32_t)(2 * (tiles < most ? tiles : most)));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  TimedLaunch t(kIdMxMatmul, st);
+  return cudaLaunchKernelEx(&cfg, k_mx_matmul_pair<FMT, BN>, maps, a);
+}
+
 template <int FMT>
 cudaError_t launch_matmul(const Operand& p, const Operand& q, uint64_t cols, const Args& a, cudaStream_t st) {
+  if (a.pairs) return launch_pairs<FMT, 256>(p, q, cols, a, st);
   if (q.rows <= 16) return launch_tiles<FMT, 16>(p, q, cols, a, st);
   if (q.rows <= 32) return launch_tiles<FMT, 32>(p, q, cols, a, st);
   if (q.rows <= 64) return launch_tiles<FMT, 64>(p, q, cols, a, st);
@@ -372,8 +686,10 @@ zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const 
     return ZIPNN_ERR_INVALID_ARG;
   if (mx_div_up(m, 128) * mx_div_up(n, 128) > 0x7FFFFFFFull) return ZIPNN_ERR_INVALID_ARG;
   if (!device_ok()) return ZIPNN_ERR_UNSUPPORTED;
-  // the longer side lies along the 128 rows of a block
-  const bool p_is_n = n >= m;
+  // Large products go to pairs of blocks, with B's rows along theirs: the sums' lanes then hold
+  // neighbours of the output. Else the longer side lies along the 128 rows of a block.
+  const bool pairs = m > 128 && n > 128 && mx_div_up(m, 256) * mx_div_up(n, 256) >= 40;
+  const bool p_is_n = pairs || n >= m;
   const Operand a{a_codes, static_cast<const uint8_t*>(a_scales), m}, b{b_codes, static_cast<const uint8_t*>(b_scales), n};
   const Operand &p = p_is_n ? b : a, &q = p_is_n ? a : b;
   Args g = {};
@@ -390,6 +706,7 @@ zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const 
   g.mmas = (uint32_t)mx_div_up(k, kMmaK);
   g.type = type;
   g.p_is_n = p_is_n;
+  g.pairs = pairs;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = format == ZIPNN_MXFP4 ? launch_matmul<kMxFp4>(p, q, k, g, st) : launch_matmul<kNvFp4>(p, q, k, g, st);
   return e == cudaSuccess ? ZIPNN_OK : ZIPNN_ERR_CUDA;

@@ -59,7 +59,8 @@ def check(mx, m, n, k, fmt, out, seed=0, exact=False):
 
 SIZES = [(1, 1, 1), (1, 128, 256), (1, 4096, 512), (3, 130, 64), (16, 256, 4096), (17, 300, 96), (32, 128, 1000), (33, 1, 40),
          (64, 640, 2048), (77, 512, 4080), (128, 128, 128), (129, 127, 31), (300, 5, 700), (200, 333, 1300), (257, 500, 33),
-         (130, 1000, 260), (512, 384, 640), (5, 2000, 11008)]
+         (130, 1000, 260), (512, 384, 640), (5, 2000, 11008), (1800, 1500, 700), (1537, 2049, 33), (2500, 1281, 1111), (10300, 100, 64),
+         (300, 5200, 2048)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
