@@ -39,6 +39,7 @@ struct Args {
   uint32_t col_tiles;          // scale tiles along a row
   uint32_t stages, mmas;       // of the whole row
   uint32_t split;              // blocks of a cluster, each a range of the stages
+  uint32_t depth, tmem_cols;
   int type, p_is_n, pairs;
 };
 
@@ -49,16 +50,26 @@ struct Shape {
   static constexpr uint32_t kP = 128 * kStageBytesK, kQ = BN * kStageBytesK;
   static constexpr uint32_t kSp = kTiles * kMxTileBytes, kSq = kSp * kHalves;
   static constexpr uint32_t kStage = (kP + kQ + kSp + kSq + 1023) / 1024 * 1024;
-  static constexpr uint32_t kDepth = BN <= 64 ? 4 : BN == 128 ? 3 : 4;
-  static constexpr uint32_t kSmem = kDepth * kStage + 1024 + 256;
+  // Stages in flight. Where the grid has more blocks than the device has SMs, two share one
+  // (100 x 32000 x 4096: 17.2 us, and 20.3 us with one block and its deeper ring); else a
+  // block has the SM's shared memory to itself (128 x 11008 x 4096: 9.6 us, and 10.8 with 3).
+  static constexpr uint32_t kShared = BN <= 64 ? 4 : 3, kAlone = BN <= 64 ? 6 : 5;
+  static constexpr uint32_t smem(uint32_t depth) { return depth * kStage + 1024 + 256; }
   // Tensor memory: the sums, and a set of scales for each stage in shared memory (4 columns a
   // tile), so that a set is written again only after the instructions that read it are done:
   // the stage's codes were not brought before that either.
   static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kHalves);
-  static constexpr uint32_t kUsed = BN + kDepth * kScaleCols;
-  static constexpr uint32_t kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static constexpr uint32_t cols(uint32_t depth) {
+    const uint32_t used = BN + depth * kScaleCols;
+    return used <= 64 ? 64 : used <= 128 ? 128 : used <= 256 ? 256 : 512;
+  }
+  static_assert(smem(kAlone) <= 227 * 1024 && BN + kAlone * kScaleCols <= 512, "one block to an SM");
+  static_assert(2 * cols(kShared) <= 512, "two blocks to an SM");
 };
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
                    smem_addr(dst)),
@@ -146,19 +157,67 @@ __device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float load_peer(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 load_peer(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
-__device__ __forceinline__ void store(const Args& a, uint32_t p, uint32_t q, float v, float g0, float g1) {
+template <typename T>
+__device__ __forceinline__ T to_value(float v) {
+  if constexpr (sizeof(T) == 4) return v;
+  else return T(v);
+}
+// N values to every `step`th place from `out`, the first n of them.
+template <typename T, int N>
+__device__ __forceinline__ void put(T* out, uint64_t step, uint32_t n, const float* v) {
+  if (n >= (uint32_t)N) {
+#pragma unroll
+    for (int c = 0; c < N; c++) out[c * step] = to_value<T>(v[c]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c++)
+      if ((uint32_t)c < n) out[c * step] = to_value<T>(v[c]);
+  }
+}
+// The sums of row p of P and rows q .. q + N - 1 of Q, scaled and rounded.
+template <int FMT, int N>
+__device__ __forceinline__ void store(const Args& a, uint32_t p, uint32_t q, float* v, float g0, float g1) {
   if (p >= a.p_rows || q >= a.q_rows) return;
-  v = v * g0 * g1;
-  const uint64_t at = a.p_is_n ? (uint64_t)q * a.ldo + p : (uint64_t)p * a.ldo + q;
-  if (a.type == kValFP32) reinterpret_cast<float*>(a.out)[at] = v;
-  else if (a.type == kValBF16) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
-  else reinterpret_cast<__half*>(a.out)[at] = __float2half_rn(v);
+  if constexpr (FMT == kNvFp4) {
+#pragma unroll
+    for (int c = 0; c < N; c++) v[c] = v[c] * g0 * g1;
+  }
+  const uint64_t at = a.p_is_n ? (uint64_t)q * a.ldo + p : (uint64_t)p * a.ldo + q, step = a.p_is_n ? a.ldo : 1;
+  if (a.type == kValFP32) put<float, N>(reinterpret_cast<float*>(a.out) + at, step, a.q_rows - q, v);
+  else if (a.type == kValBF16) put<__nv_bfloat16, N>(reinterpret_cast<__nv_bfloat16*>(a.out) + at, step, a.q_rows - q, v);
+  else put<__half, N>(reinterpret_cast<__half*>(a.out) + at, step, a.q_rows - q, v);
+}
+
+// The sums of a block of a cluster lie in its shared memory as (columns / 4, 128 rows, 4).
+// This block's share of the columns of this thread's row: every SPLIT-th four, added over the
+// blocks in their order. Eight loads are in flight at a time (each takes a good part of a
+// microsecond).
+template <int FMT, int SPLIT>
+__device__ __forceinline__ void add_peers(const Args& a, const float4* sums, uint32_t rank, uint32_t used, uint32_t p, uint32_t q,
+                                          float g0, float g1) {
+  constexpr uint32_t kAtOnce = 8 / SPLIT;
+  for (uint32_t c = rank * 4; c < used; c += kAtOnce * SPLIT * 4) {
+    float4 t[kAtOnce][SPLIT];
+#pragma unroll
+    for (uint32_t k = 0; k < kAtOnce; k++)
+#pragma unroll
+      for (int r = 0; r < SPLIT; r++)
+        if (c + k * SPLIT * 4 < used) t[k][r] = load_peer(peer(smem_addr(sums + (c / 4 + k * SPLIT) * 128 + threadIdx.x), r));
+#pragma unroll
+    for (uint32_t k = 0; k < kAtOnce; k++) {
+      if (c + k * SPLIT * 4 >= used) break;
+      float4 v = t[k][0];
+#pragma unroll
+      for (int r = 1; r < SPLIT; r++) v.x += t[k][r].x, v.y += t[k][r].y, v.z += t[k][r].z, v.w += t[k][r].w;
+      store<FMT, 4>(a, p, q + c + k * SPLIT * 4, &v.x, g0, g1);
+    }
+  }
 }
 
 template <int FMT, int BN>
@@ -167,26 +226,48 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   using S = Shape<FMT, BN>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kDepth * S::kStage);
-  uint64_t *empty = full + S::kDepth, *done = empty + S::kDepth;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.depth * S::kStage);
+  uint64_t *empty = full + a.depth, *done = empty + a.depth;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
   volatile uint32_t* failed = tmem_at + 1;
 
-  const uint32_t warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+  const uint32_t warp = uniform(threadIdx.x / 32);
   const uint32_t tile = blockIdx.x / a.split, rank = blockIdx.x % a.split;
   const uint32_t p0 = tile / a.q_tiles * 128, q0 = tile % a.q_tiles * BN;
   const uint32_t lo = (uint32_t)((uint64_t)a.stages * rank / a.split), hi = (uint32_t)((uint64_t)a.stages * (rank + 1) / a.split);
 
-  if (warp == 4 && lane == 0) {
-    for (uint32_t i = 0; i < S::kDepth; i++) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+  // Stage i of the row into place `at` of the ring. Scale tiles that the row does not have are
+  // not brought.
+  const auto bring = [&](uint32_t i, uint32_t at) {
+    const uint32_t halves = S::kHalves == 2 && q0 + 128 < a.q_rows ? 2 : 1;
+    uint8_t* st = smem + at * S::kStage;
+    uint64_t* bar = full + at;
+    const uint32_t t0 = i * S::kTiles, bytes = min(S::kTiles, a.col_tiles - t0) * kMxTileBytes;
+    mbar_expect_tx(bar, S::kP + S::kQ + bytes * (1 + halves));
+    tma_2d(st, &p_map, (int32_t)(i * kStageBytesK), (int32_t)p0, bar);
+    tma_2d(st + S::kP, &q_map, (int32_t)(i * kStageBytesK), (int32_t)q0, bar);
+    uint8_t* sc = st + S::kP + S::kQ;
+    bulk_g2s(sc, a.p_scales + ((uint64_t)(p0 / 128) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
+    for (uint32_t h = 0; h < halves; h++)
+      bulk_g2s(sc + S::kSp + h * S::kSp, a.q_scales + ((uint64_t)(q0 / 128 + h) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
+  };
+  const uint32_t early = min(hi - lo, a.depth);  // stages brought before the block has met
+  if (warp == 4) {
+    if (elect()) {
+      prefetch_map(&p_map);
+      prefetch_map(&q_map);
+      for (uint32_t i = 0; i < a.depth; i++) {
+        mbar_init(full + i, 1);
+        mbar_init(empty + i, 1);
+      }
+      mbar_init(done, 1);
+      *failed = 0;
+      for (uint32_t i = 0; i < early; i++) bring(lo + i, i);
     }
-    mbar_init(done, 1);
-    *failed = 0;
+    __syncwarp();
   }
   if (warp == 5) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_at)), "r"(S::kCols) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_at)), "r"(a.tmem_cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -196,32 +277,20 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
 
   if (warp == 4) {
     const bool one = elect();
-    const uint32_t halves = S::kHalves == 2 && q0 + 128 < a.q_rows ? 2 : 1;
     Ring r;
-    for (uint32_t i = lo; i < hi; i++, r.next(S::kDepth)) {
-      if (i - lo >= S::kDepth && !mbar_wait_bounded(empty + r.at, r.parity ^ 1, kWaitPolls)) {
+    for (uint32_t i = lo + early; i < hi; i++, r.next(a.depth)) {
+      if (!mbar_wait_bounded(empty + r.at, r.parity, kWaitPolls)) {
         *failed = 1;
         break;
       }
-      if (one) {
-        uint8_t* st = smem + r.at * S::kStage;
-        uint64_t* bar = full + r.at;
-        const uint32_t t0 = i * S::kTiles, bytes = min(S::kTiles, a.col_tiles - t0) * kMxTileBytes;
-        mbar_expect_tx(bar, S::kP + S::kQ + bytes * (1 + halves));
-        tma_2d(st, &p_map, (int32_t)(i * kStageBytesK), (int32_t)p0, bar);
-        tma_2d(st + S::kP, &q_map, (int32_t)(i * kStageBytesK), (int32_t)q0, bar);
-        uint8_t* sc = st + S::kP + S::kQ;
-        bulk_g2s(sc, a.p_scales + ((uint64_t)(p0 / 128) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
-        for (uint32_t h = 0; h < halves; h++)
-          bulk_g2s(sc + S::kSp + h * S::kSp, a.q_scales + ((uint64_t)(q0 / 128 + h) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
-      }
+      if (one) bring(i, r.at);
       __syncwarp();
     }
   } else if (warp == 5) {
     const bool one = elect();
     Ring r;
     uint32_t left = a.mmas - lo * (kStageK / kMmaK);  // instructions to the end of the row
-    for (uint32_t i = lo; i < hi; i++, r.next(S::kDepth), left -= kStageK / kMmaK) {
+    for (uint32_t i = lo; i < hi; i++, r.next(a.depth), left -= kStageK / kMmaK) {
       if (!mbar_wait_bounded(full + r.at, r.parity, kWaitPolls)) {
         *failed = 1;
         break;
@@ -261,35 +330,35 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   }
   const bool ok = *failed == 0;
   const float g0 = FMT == kNvFp4 ? *a.ga : 1.f, g1 = FMT == kNvFp4 ? *a.gb : 1.f;
+  const uint32_t used = min((uint32_t)BN, a.q_rows - q0);  // columns that the output has
   if (a.split == 1) {
     if (warp < 4 && ok) {
-      for (uint32_t c = 0; c < (uint32_t)BN; c += 16) {
-        if (q0 + c >= a.q_rows) break;
+#pragma unroll 1
+      for (uint32_t c = 0; c < used; c += 16) {
         float v[16];
         load_sums(tmem + (warp * 32 << 16) + c, v);
-#pragma unroll
-        for (int i = 0; i < 16; i++) store(a, p0 + threadIdx.x, q0 + c + i, v[i], g0, g1);
+        store<FMT, 16>(a, p0 + threadIdx.x, q0 + c, v, g0, g1);
       }
     }
   } else {
     // each block's sums to its shared memory (its stages are spent), then every block adds its
-    // share of the columns over the cluster, in the blocks' order
-    float* sums = reinterpret_cast<float*>(smem);
+    // share of the columns over the cluster
+    float4* sums = reinterpret_cast<float4*>(smem);
     if (warp < 4) {
-      for (uint32_t c = 0; c < (uint32_t)BN; c += 16) {
+#pragma unroll 1
+      for (uint32_t c = 0; c < used; c += 16) {
         float v[16];
         load_sums(tmem + (warp * 32 << 16) + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; i++) sums[(c + i) * 128 + threadIdx.x] = v[i];
+        for (int i = 0; i < 16; i += 4) sums[(c + i) / 4 * 128 + threadIdx.x] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
     cluster_sync();
     if (warp < 4 && ok) {
-      for (uint32_t c = rank; c < (uint32_t)BN && q0 + c < a.q_rows; c += a.split) {
-        float v = 0.f;
-        for (uint32_t r = 0; r < a.split; r++) v += load_peer(peer(smem_addr(sums + c * 128 + threadIdx.x), r));
-        store(a, p0 + threadIdx.x, q0 + c, v, g0, g1);
-      }
+      const uint32_t p = p0 + threadIdx.x;
+      if (a.split == 2) add_peers<FMT, 2>(a, sums, rank, used, p, q0, g0, g1);
+      else if (a.split == 4) add_peers<FMT, 4>(a, sums, rank, used, p, q0, g0, g1);
+      else add_peers<FMT, 8>(a, sums, rank, used, p, q0, g0, g1);
     }
     cluster_sync();
   }
@@ -297,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   __syncthreads();
   if (warp == 5) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.tmem_cols));
   }
 }
 
@@ -376,23 +445,6 @@ __device__ __forceinline__ void load_sums32(uint32_t taddr, float* v) {
       : "r"(taddr));
 }
 
-template <typename T>
-__device__ __forceinline__ T to_value(float v) {
-  if constexpr (sizeof(T) == 4) return v;
-  else return T(v);
-}
-template <typename T, int N>
-__device__ __forceinline__ void store_column(T* out, uint64_t ldo, uint32_t n, const float* v) {
-  if (n >= (uint32_t)N) {
-#pragma unroll
-    for (int c = 0; c < N; c++) out[c * ldo] = to_value<T>(v[c]);
-  } else {
-#pragma unroll
-    for (int c = 0; c < N; c++)
-      if ((uint32_t)c < n) out[c * ldo] = to_value<T>(v[c]);
-  }
-}
-
 struct PairMaps {
   CUtensorMap p, q, sp, sq;
 };
@@ -411,14 +463,32 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
   const uint32_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const uint32_t tiles = (a.p_rows + 255) / 256 * a.q_tiles;
 
-  if (warp == 8 && lane == 0) {
-    for (uint32_t i = 0; i < S::kDepth; i++) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+  // Stage i of a tile into place `at` of the ring: this block's share, whose bytes count at the
+  // first block's barrier with the other's.
+  const auto bring = [&](uint32_t t, uint32_t i, uint32_t at) {
+    const uint32_t p0 = t / a.q_tiles * 256 + rank * 128, q0 = t % a.q_tiles * BN;
+    if (rank == 0) mbar_expect_tx(full + at, 2 * S::kBytes);
+    const uint32_t st = smem_addr(smem) + at * S::kStage, bar = peer(smem_addr(full + at), 0);
+    tma_pair_2d(st, &maps.p, (int32_t)(i * kStageBytesK), (int32_t)p0, bar);
+    tma_pair_2d(st + S::kP, &maps.q, (int32_t)(i * kStageBytesK), (int32_t)(q0 + rank * (BN / 2)), bar);
+    tma_pair_3d(st + S::kP + S::kQ, &maps.sp, 0, (int32_t)(i * S::kTiles), (int32_t)(p0 / 128), bar);
+    tma_pair_3d(st + S::kP + S::kQ + S::kSp, &maps.sq, 0, (int32_t)(i * S::kTiles), (int32_t)(q0 / 128), bar);
+  };
+  if (warp == 8) {
+    if (elect()) {
+      prefetch_map(&maps.p);
+      prefetch_map(&maps.q);
+      prefetch_map(&maps.sp);
+      prefetch_map(&maps.sq);
+      for (uint32_t i = 0; i < S::kDepth; i++) {
+        mbar_init(full + i, 1);
+        mbar_init(empty + i, 1);
+      }
+      mbar_init(sums_full, 1);
+      mbar_init(sums_empty, 16);  // eight warps of two blocks
+      *failed = 0;
     }
-    mbar_init(sums_full, 1);
-    mbar_init(sums_empty, 16);  // eight warps of two blocks
-    *failed = 0;
+    __syncwarp();
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_at)), "r"(512u) : "memory");
@@ -435,21 +505,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
     Ring r;
     uint32_t n = 0;  // stages brought so far
     for (uint32_t t = pair; t < tiles && !*failed; t += pairs) {
-      const uint32_t p0 = t / a.q_tiles * 256 + rank * 128, q0 = t % a.q_tiles * BN;
       for (uint32_t i = 0; i < a.stages; i++, n++, r.next(S::kDepth)) {
         if (n >= S::kDepth && !mbar_wait_bounded(empty + r.at, r.parity ^ 1, kWaitPolls)) {
           *failed = 1;
           break;
         }
-        if (one) {
-          // both blocks' bytes count at the first one's barrier
-          if (rank == 0) mbar_expect_tx(full + r.at, 2 * S::kBytes);
-          const uint32_t st = smem_addr(smem) + r.at * S::kStage, bar = peer(smem_addr(full + r.at), 0);
-          tma_pair_2d(st, &maps.p, (int32_t)(i * kStageBytesK), (int32_t)p0, bar);
-          tma_pair_2d(st + S::kP, &maps.q, (int32_t)(i * kStageBytesK), (int32_t)(q0 + rank * (BN / 2)), bar);
-          tma_pair_3d(st + S::kP + S::kQ, &maps.sp, 0, (int32_t)(i * S::kTiles), (int32_t)(p0 / 128), bar);
-          tma_pair_3d(st + S::kP + S::kQ + S::kSp, &maps.sq, 0, (int32_t)(i * S::kTiles), (int32_t)(q0 / 128), bar);
-        }
+        if (one) bring(t, i, r.at);
         __syncwarp();
       }
     }
@@ -517,17 +578,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive_at(leader_bar);
-      if (p < a.p_rows && q < a.q_rows && !*failed) {
-        const uint32_t cols = a.q_rows - q;
-        if constexpr (FMT == kNvFp4) {
-#pragma unroll
-          for (int c = 0; c < kCols; c++) v[c] = v[c] * g * g1;
-        }
-        const uint64_t at = (uint64_t)q * a.ldo + p;
-        if (a.type == kValFP32) store_column<float, kCols>(reinterpret_cast<float*>(a.out) + at, a.ldo, cols, v);
-        else if (a.type == kValBF16) store_column<__nv_bfloat16, kCols>(reinterpret_cast<__nv_bfloat16*>(a.out) + at, a.ldo, cols, v);
-        else store_column<__half, kCols>(reinterpret_cast<__half*>(a.out) + at, a.ldo, cols, v);
-      }
+      if (!*failed) store<FMT, kCols>(a, p, q, v, g, g1);
     }
     __syncwarp();
   }
@@ -571,6 +622,11 @@ bool code_map(CUtensorMap* m, const void* codes, uint64_t rows, uint64_t row_byt
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaError_t device_sms(int& dev, int& sms) {
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
 struct Operand {
   const void* codes;
   const uint8_t* scales;
@@ -581,11 +637,11 @@ template <int FMT, int BN>
 cudaError_t launch_tiles(const Operand& p, const Operand& q, uint64_t cols, Args a, cudaStream_t st) {
   using S = Shape<FMT, BN>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_mx_matmul<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    e = cudaFuncSetAttribute(k_mx_matmul<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem(S::kAlone));
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -594,13 +650,17 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, uint64_t cols, Args
   if (!code_map(&pm, p.codes, p.rows, rb, 128) || !code_map(&qm, q.codes, q.rows, rb, BN)) return cudaErrorUnknown;
   const uint64_t q_tiles = mx_div_up(q.rows, BN), tiles = mx_div_up(p.rows, 128) * q_tiles;
   a.q_tiles = (uint32_t)q_tiles;
+  // As many blocks to a tile as leave each an SM of its own (16 x 4096 x 4096, 32 tiles: 6.3 us
+  // unsplit, 5.4 by 4, 6.7 by 8; 64 x 11008 x 4096, 86 tiles: 8.5 unsplit, 10.0 by 2).
   a.split = 1;
-  while (a.split < 8 && tiles * a.split * 2 <= 2 * 148 && a.split * 2 <= a.stages) a.split *= 2;
+  while (a.split < 8 && tiles * a.split * 2 <= (uint64_t)sms && a.split * 2 <= a.stages) a.split *= 2;
+  a.depth = tiles * a.split <= (uint64_t)sms ? S::kAlone : S::kShared;
+  a.tmem_cols = S::cols(a.depth);
   if (tiles * a.split > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((uint32_t)(tiles * a.split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.dynamicSmemBytes = S::smem(a.depth);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -627,8 +687,7 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, uint64_t cols, Args
   using S = PairShape<FMT, BN>;
   static std::atomic<uint64_t> ready{0};
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
     e = cudaFuncSetAttribute(k_mx_matmul_pair<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
@@ -686,10 +745,12 @@ zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const 
     return ZIPNN_ERR_INVALID_ARG;
   if (mx_div_up(m, 128) * mx_div_up(n, 128) > 0x7FFFFFFFull) return ZIPNN_ERR_INVALID_ARG;
   if (!device_ok()) return ZIPNN_ERR_UNSUPPORTED;
-  // Large products go to pairs of blocks, with B's rows along theirs: the sums' lanes then hold
-  // neighbours of the output. Else the longer side lies along the 128 rows of a block.
+  // Large products go to pairs of blocks (1024 x 4096 x 4096, 64 tiles: 11.6 us, 12.7 by single
+  // blocks; 512 x 4096 x 4096, 32 tiles: 10.8 and 9.0). B's rows lie along the 128 rows of a
+  // block, whose lanes then hold neighbours of the output (4096 x 256 x 4096: 9 us, 19 with A's),
+  // unless they are few and A's are more.
   const bool pairs = m > 128 && n > 128 && mx_div_up(m, 256) * mx_div_up(n, 256) >= 40;
-  const bool p_is_n = pairs || n >= m;
+  const bool p_is_n = n >= 128 || n >= m;
   const Operand a{a_codes, static_cast<const uint8_t*>(a_scales), m}, b{b_codes, static_cast<const uint8_t*>(b_scales), n};
   const Operand &p = p_is_n ? b : a, &q = p_is_n ? a : b;
   Args g = {};
