@@ -23,6 +23,7 @@ constexpr uint32_t kChunkVecs = 1024;   // 16 KB of one page are one unit of the
 // written by every call that uses them.
 struct Head {
   uint32_t status, live, pairs, refused;
+  unsigned long long next;  // units of the copy that blocks have taken
 };
 
 struct Request {
@@ -51,33 +52,59 @@ __device__ __forceinline__ void let_dependents_start() { asm volatile("griddepco
 // without a list; a negative number skips the pair), in every plane. A unit is 16 KB of one
 // page of one plane; short pages share a block, a power of two of threads for each. Each
 // thread holds up to four 16-byte vectors between its loads and its stores.
-__device__ void copy_units(const Pool& src, const int32_t* src_ids, const Pool& dst, const int32_t* dst_ids,
-                           uint32_t count, uint32_t planes, uint32_t page_vecs, Head* head) {
-  const uint32_t chunks = (page_vecs + kChunkVecs - 1) / kChunkVecs;
-  uint32_t tpu = 1;  // threads of a unit
-  while (tpu < page_vecs && tpu < kCopyThreads) tpu <<= 1;
-  const uint32_t per_block = kCopyThreads / tpu, lane = threadIdx.x & (tpu - 1);
-  const uint64_t units = (uint64_t)planes * count * chunks;
-  for (uint64_t u = (uint64_t)blockIdx.x * per_block + threadIdx.x / tpu; u < units; u += (uint64_t)gridDim.x * per_block) {
-    const uint64_t q = u / chunks;
-    const uint32_t chunk = (uint32_t)(u - q * chunks);
-    const uint32_t plane = (uint32_t)(q / count), i = (uint32_t)(q - (uint64_t)plane * count);
-    const int64_t s = src_ids ? src_ids[i] : (int64_t)i, d = dst_ids ? dst_ids[i] : (int64_t)i;
-    if (s < 0 || d < 0) continue;
-    if (s >= src.pages || d >= dst.pages) {
-      set_status(head, kStInvalid);
-      continue;
-    }
-    const uint4* from = reinterpret_cast<const uint4*>(src.base + plane * src.plane_stride + s * src.page_stride);
-    uint4* to = reinterpret_cast<uint4*>(dst.base + plane * dst.plane_stride + d * dst.page_stride);
-    const uint32_t lo = chunk * kChunkVecs + lane, hi = min(page_vecs, (chunk + 1) * kChunkVecs);
-    uint4 v[kChunkVecs / kCopyThreads];
+struct Units {
+  uint32_t chunks, tpu, per_block, lane;  // units of a page and plane; threads of a unit; units of a block; this thread in its unit
+  uint64_t all;
+  __device__ __forceinline__ Units(uint32_t count, uint32_t planes, uint32_t page_vecs) {
+    chunks = (page_vecs + kChunkVecs - 1) / kChunkVecs;
+    tpu = 1;
+    while (tpu < page_vecs && tpu < kCopyThreads) tpu <<= 1;
+    per_block = kCopyThreads / tpu;
+    lane = threadIdx.x & (tpu - 1);
+    all = (uint64_t)planes * count * chunks;
+  }
+};
+
+// The units of this block, `first` being the number of its first one.
+__device__ __forceinline__ void copy_unit(const Units& n, uint64_t first, const Pool& src, const int32_t* src_ids, const Pool& dst,
+                                          const int32_t* dst_ids, uint32_t count, uint32_t page_vecs, Head* head) {
+  const uint64_t u = first + threadIdx.x / n.tpu;
+  if (u >= n.all) return;
+  const uint64_t q = u / n.chunks;
+  const uint32_t chunk = (uint32_t)(u - q * n.chunks);
+  const uint32_t plane = (uint32_t)(q / count), i = (uint32_t)(q - (uint64_t)plane * count);
+  const int64_t s = src_ids ? src_ids[i] : (int64_t)i, d = dst_ids ? dst_ids[i] : (int64_t)i;
+  if (s < 0 || d < 0) return;
+  if (s >= src.pages || d >= dst.pages) {
+    set_status(head, kStInvalid);
+    return;
+  }
+  const uint4* from = reinterpret_cast<const uint4*>(src.base + plane * src.plane_stride + s * src.page_stride);
+  uint4* to = reinterpret_cast<uint4*>(dst.base + plane * dst.plane_stride + d * dst.page_stride);
+  const uint32_t lo = chunk * kChunkVecs + n.lane, hi = min(page_vecs, (chunk + 1) * kChunkVecs);
+  uint4 v[kChunkVecs / kCopyThreads];
 #pragma unroll
-    for (int k = 0; k < (int)(kChunkVecs / kCopyThreads); k++)
-      if (lo + k * tpu < hi) v[k] = from[lo + k * tpu];
+  for (int k = 0; k < (int)(kChunkVecs / kCopyThreads); k++)
+    if (lo + k * n.tpu < hi) v[k] = from[lo + k * n.tpu];
 #pragma unroll
-    for (int k = 0; k < (int)(kChunkVecs / kCopyThreads); k++)
-      if (lo + k * tpu < hi) to[lo + k * tpu] = v[k];
+  for (int k = 0; k < (int)(kChunkVecs / kCopyThreads); k++)
+    if (lo + k * n.tpu < hi) to[lo + k * n.tpu] = v[k];
+}
+
+// Within one pool, where the number of pairs was found on the device: the blocks take the next
+// units as they get done, in the order of memory (head->next starts at 0).
+__device__ __forceinline__ void copy_pairs(const Pool& pool, const int32_t* src_ids, const int32_t* dst_ids, uint32_t count,
+                                           uint32_t planes, uint32_t page_vecs, Head* head) {
+  __shared__ unsigned long long taken[2];
+  const Units n(count, planes, page_vecs);
+  if (threadIdx.x == 0) taken[0] = n.all ? atomicAdd(&head->next, (unsigned long long)n.per_block) : 0;
+  __syncthreads();
+  for (uint32_t turn = 0;; turn ^= 1) {
+    const uint64_t u = taken[turn];
+    if (u >= n.all) break;
+    if (threadIdx.x == 0) taken[turn ^ 1] = atomicAdd(&head->next, (unsigned long long)n.per_block);
+    copy_unit(n, u, pool, src_ids, pool, dst_ids, count, page_vecs, head);
+    __syncthreads();
   }
 }
 
@@ -88,7 +115,9 @@ __global__ void __launch_bounds__(kCopyThreads) k_pages_copy(Pool src, const int
     wait_for_plan();
     if (*reinterpret_cast<volatile uint32_t*>(&head->refused)) return;
   }
-  copy_units(src, src_ids, dst, dst_ids, count, planes, page_vecs, head);
+  const Units n(count, planes, page_vecs);
+  for (uint64_t u = (uint64_t)blockIdx.x * n.per_block; u < n.all; u += (uint64_t)gridDim.x * n.per_block)
+    copy_unit(n, u, src, src_ids, dst, dst_ids, count, page_vecs, head);
 }
 
 // Before a copy that could write a page twice, or one that it also reads: every number in its
@@ -248,6 +277,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan_fork(Meta m, const 
   if (threadIdx.x == 0) {
     head->refused = 0;
     head->pairs = pairs;
+    head->next = 0;
   }
 }
 
@@ -275,7 +305,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_pages_fork(Meta m, Pool pool, 
     }
     if (threadIdx.x == 0) m.lens[r.row] = (int32_t)r.len;
   }
-  copy_units(pool, pair_src, pool, pair_dst, *reinterpret_cast<volatile uint32_t*>(&head->pairs), planes, page_vecs, head);
+  copy_pairs(pool, pair_src, pair_dst, *reinterpret_cast<volatile uint32_t*>(&head->pairs), planes, page_vecs, head);
 }
 
 // A block to a row: its pages lose a reference each, its slots and its length are cleared. The
@@ -348,6 +378,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_plan_compact(Meta m, Hea
   if (threadIdx.x == 0) {
     head->live = live;
     head->pairs = live - below;
+    head->next = 0;
   }
 }
 
@@ -371,7 +402,7 @@ __global__ void __launch_bounds__(kCopyThreads) k_pages_compact(Meta m, Pool poo
     m.refs[pair_dst[i]] = m.refs[pair_src[i]];
     m.refs[pair_src[i]] = 0;
   }
-  copy_units(pool, pair_src, pool, pair_dst, pairs, planes, page_vecs, head);
+  copy_pairs(pool, pair_src, pair_dst, pairs, planes, page_vecs, head);
 }
 
 template <typename... P, typename... A>
@@ -388,12 +419,17 @@ cudaError_t launch(void (*kernel)(P...), uint32_t grid, bool dependent, cudaStre
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-uint32_t copy_grid(uint64_t count, uint32_t planes, uint64_t page_vecs) {
+// Blocks for the copy of at most `count` pages. A block that takes one unit and ends, the next
+// starting in its place, copies faster than one that walks over many (1.34 GB in 32 KB pages,
+// scattered: 390 us with a block a unit, 411 with 148 x 64 blocks, 438 with 148 x 8). Where the
+// number of pages is found on the device and may be far below `count`, empty blocks would cost
+// more than that: `most` blocks then take units in turn (copy_pairs).
+uint32_t copy_grid(uint64_t count, uint32_t planes, uint64_t page_vecs, uint64_t most = 0x7FFFFFFF) {
   uint64_t tpu = 1;
   while (tpu < page_vecs && tpu < (uint64_t)kCopyThreads) tpu <<= 1;
   const uint64_t units = (uint64_t)planes * count * ((page_vecs + kChunkVecs - 1) / kChunkVecs);
-  const uint64_t blocks = (units * tpu + kCopyThreads - 1) / kCopyThreads;
-  return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(blocks, 148 * 8));
+  const uint64_t per_block = kCopyThreads / tpu, blocks = units / per_block + (units % per_block != 0);
+  return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(blocks, most));
 }
 
 inline bool bad16(const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
@@ -422,6 +458,7 @@ uint64_t pool_end(const zipnn_page_pool* p, uint64_t page_bytes) {
 
 Pool device_pool(const zipnn_page_pool* p) { return Pool{static_cast<uint8_t*>(p->base), p->plane_stride, p->page_stride, p->pages}; }
 
+constexpr uint64_t kTakers = 148 * 4;  // 122 us for 174 pages of 2 MB; 124 with 148 x 6, 126 with 148 x 8
 constexpr uint64_t kHeadBytes = 256;
 uint64_t align256(uint64_t x) { return (x + 255) & ~255ull; }
 
@@ -509,7 +546,7 @@ zipnn_status zipnn_pages_fork(const zipnn_page_pool* pool, uint64_t page_bytes, 
   if (e == cudaSuccess) {
     TimedLaunch t(kIdPagesMove, st);
     const uint32_t vecs = (uint32_t)(page_bytes / 16);
-    const uint32_t grid = std::max(std::min(count, 148u * 8), copy_grid(count, pool->planes, vecs));
+    const uint32_t grid = std::max<uint32_t>(std::min<uint32_t>(count, kTakers), copy_grid(count, pool->planes, vecs, kTakers));
     e = launch(k_pages_fork, grid, true, st, m, device_pool(pool), pool->planes, vecs, count, head, req, fresh, ps, pd);
   }
   return cuda_status(e);
@@ -545,7 +582,7 @@ zipnn_status zipnn_pages_free(const zipnn_page_pool* pool, uint64_t page_bytes, 
   if (e == cudaSuccess && compact) {
     TimedLaunch t(kIdPagesMove, st);
     const uint32_t vecs = (uint32_t)(page_bytes / 16);
-    e = launch(k_pages_compact, copy_grid(pool->pages / 2 + 1, pool->planes, vecs), true, st, m, device_pool(pool), pool->planes, vecs,
+    e = launch(k_pages_compact, copy_grid(pool->pages / 2 + 1, pool->planes, vecs, kTakers), true, st, m, device_pool(pool), pool->planes, vecs,
                head, to, ps, pd);
   }
   return cuda_status(e);
