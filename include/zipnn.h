@@ -310,6 +310,7 @@ zipnn_status zipnn_shard_tables(zipnn_dtype dtype, uint32_t chunk_bytes, uint32_
  * 512 * (row / 128 * ceil(blocks / 4) + block / 4), row-and-block at
  * 16 * (row % 32) + 4 * (row / 32 % 4) + block % 4 in it: the order in which the tensor cores
  * take them. Bytes of rows and blocks past the matrix are zero; every call reads them so.
+ * At most 2^31 rows, 2^30 columns, and row strides of 2^40 values.
  * Device pointers are 16-byte aligned except where a call says otherwise. */
 typedef enum { ZIPNN_MXFP4 = 0, ZIPNN_NVFP4 = 1 } zipnn_mx_format;
 /* Types of plain values (not those of zipnn_dtype: FP16 is not a type of the codec). */

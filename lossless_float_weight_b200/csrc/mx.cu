@@ -29,9 +29,18 @@ struct Cover {
 };
 
 Cover cover(uint64_t rows, uint64_t chunks, uint32_t most) {
+  // The widest block that leaves at most an eighth of its threads past the row's end, or the
+  // one of at least 4 chunks that leaves the fewest (11008 x 4097, 129 chunks a row: 32 us with
+  // blocks of 128 or 256, 23 with 32).
   Cover c;
+  uint64_t fewest = ~0ull;
   c.log_cols = 0;
-  while ((1ull << c.log_cols) < chunks && (1 << c.log_cols) < kThreads) c.log_cols++;
+  for (uint32_t l = 8; l >= 2; l--) {
+    if (l > 2 && (1ull << (l - 1)) >= chunks) continue;
+    const uint64_t padded = mx_div_up(chunks, 1ull << l) << l;
+    if (padded < fewest) fewest = padded, c.log_cols = l;
+    if (padded - chunks <= chunks / 8) break;
+  }
   c.col_tiles = (uint32_t)mx_div_up(chunks, 1ull << c.log_cols);
   c.row_tiles = (uint32_t)mx_div_up(rows, (uint64_t)kThreads >> c.log_cols);
   const uint32_t down = most / c.col_tiles;
@@ -484,56 +493,59 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize(Packed m, uint8_t* o
   }
 }
 
-// Rows that start anywhere: one thread writes one aligned 16-byte vector of the output (8 or 4
-// values), and it is the codes, 4 bits each, that are shifted into place. The vector lies in at
-// most two blocks.
+// Rows that start anywhere: one thread writes 16 values from a 16-byte boundary of the output
+// on, as whole vectors but at a row's ends, and it is the codes, 4 bits each, that are shifted
+// into place. The values lie in at most two blocks.
 template <int FMT, int TYPE>
 __global__ void __launch_bounds__(kThreads) k_mx_dequantize_any(Packed m, uint8_t* out, uint64_t stride_bytes, Cover c) {
   constexpr int B = (int)mx_value_bytes(TYPE), V = 16 / B;
-  constexpr uint32_t kBlk = mx_block(FMT);
+  constexpr int kBlk = (int)mx_block(FMT);
   const float g = FMT == kNvFp4 ? *m.global_scale : 1.f;
-  const int64_t cols = m.cols;
+  const int cols = (int)m.cols, words = (int)(m.row_bytes / 4);
   Walk at(c);
   for (; at.tile < c.row_tiles; at.tile += at.tile_step) {
     const uint32_t row = at.row();
     if (row >= m.rows) break;
     uint8_t* o = out + row * stride_bytes;
-    const int64_t e0 = (int64_t)at.chunk * V - (int64_t)((reinterpret_cast<uintptr_t>(o) & 15) / B);
+    const int e0 = (int)at.chunk * kReadBack - (int)((uint32_t)reinterpret_cast<uintptr_t>(o) & 15) / B;
     if (e0 >= cols) continue;
-    const int64_t lo = e0 < 0 ? 0 : e0, hi = e0 + V < cols ? e0 + V : cols;  // values lo .. hi - 1
+    const int lo = max(e0, 0), hi = min(e0 + kReadBack, cols);  // values lo .. hi - 1
     const uint32_t* w = reinterpret_cast<const uint32_t*>(m.codes + row * m.row_bytes);
-    const int64_t w0 = e0 >> 3;
+    const int w0 = e0 >> 3;
     const uint32_t sh = 4 * (uint32_t)(e0 & 7);
-    uint32_t bits = w0 >= 0 ? __ldg(w + w0) : 0u;
-    if (sh + 4 * V > 32) bits = __funnelshift_r(bits, (uint64_t)(w0 + 1) * 4 < m.row_bytes ? __ldg(w + w0 + 1) : 0u, sh);
-    else bits >>= sh;
-    const uint32_t b0 = (uint32_t)lo / kBlk, b1 = (uint32_t)(hi - 1) / kBlk;
+    const uint32_t c0 = w0 >= 0 ? __ldg(w + w0) : 0u, c1 = w0 + 1 < words ? __ldg(w + w0 + 1) : 0u;
+    const uint32_t c2 = sh && w0 + 2 < words ? __ldg(w + w0 + 2) : 0u;
+    const uint32_t bits[2] = {__funnelshift_r(c0, c1, sh), __funnelshift_r(c1, c2, sh)};
+    const int b0 = lo / kBlk, b1 = (hi - 1) / kBlk;
     const uint8_t* st = m.scales + row / 128 * m.col_tiles * kMxTileBytes + mx_in_tile(row % 128, 0);
-    const float s0 = scale_of<FMT>(__ldg(st + (uint64_t)(b0 / 4) * kMxTileBytes + b0 % 4));
-    const float s1 = b1 == b0 ? s0 : scale_of<FMT>(__ldg(st + (uint64_t)(b1 / 4) * kMxTileBytes + b1 % 4));
-    const int cut = (int)((int64_t)(b0 + 1) * kBlk - e0);  // values from here on are of the second block
-    float v[V];
+    const float s0 = scale_of<FMT>(__ldg(st + (uint32_t)(b0 / 4) * kMxTileBytes + b0 % 4));
+    const float s1 = b1 == b0 ? s0 : scale_of<FMT>(__ldg(st + (uint32_t)(b1 / 4) * kMxTileBytes + b1 % 4));
+    const int cut = (b0 + 1) * kBlk - e0;  // values from here on are of the second block
+    float v[kReadBack];
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 f = two_values(bits, i);
+    for (int i = 0; i < kReadBack; i += 2) {
+      const float2 f = two_values(bits[i / 8], i % 8);
       v[i] = f.x * (i < cut ? s0 : s1);
       v[i + 1] = f.y * (i + 1 < cut ? s0 : s1);
     }
     if constexpr (FMT == kNvFp4) {
 #pragma unroll
-      for (int i = 0; i < V; i++) v[i] *= g;
+      for (int i = 0; i < kReadBack; i++) v[i] *= g;
     }
-    const uint4 p = pack_values<TYPE>(v);
-    uint8_t* to = o + e0 * B;
-    if (lo == e0 && hi == e0 + V) {
-      *reinterpret_cast<uint4*>(to) = p;
-    } else {
-      const uint32_t words[4] = {p.x, p.y, p.z, p.w};
+    uint8_t* to = o + (int64_t)e0 * B;
 #pragma unroll
-      for (int i = 0; i < V; i++) {
-        if (e0 + i < lo || e0 + i >= hi) continue;
-        if constexpr (B == 4) reinterpret_cast<uint32_t*>(to)[i] = words[i];
-        else reinterpret_cast<uint16_t*>(to)[i] = (uint16_t)(words[i / 2] >> (16 * (i % 2)));
+    for (int k = 0; k < kReadBack; k += V) {
+      const uint4 p = pack_values<TYPE>(v + k);
+      if (e0 + k >= lo && e0 + k + V <= hi) {
+        *reinterpret_cast<uint4*>(to + k * B) = p;
+      } else {
+        const uint32_t word[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          if (e0 + k + i < lo || e0 + k + i >= hi) continue;
+          if constexpr (B == 4) reinterpret_cast<uint32_t*>(to)[k + i] = word[i];
+          else reinterpret_cast<uint16_t*>(to)[k + i] = (uint16_t)(word[i / 2] >> (16 * (i % 2)));
+        }
       }
     }
   }
@@ -568,8 +580,8 @@ cudaError_t launch_dequantize(const Packed& m, uint8_t* out, uint64_t stride_byt
     const Cover c = cover(m.rows, mx_div_up(m.cols, kReadBack), kGrid);
     k_mx_dequantize<FMT, TYPE><<<c.grid, kThreads, 0, st>>>(m, out, stride_bytes, c);
   } else {
-    // a row that starts off a boundary has a vector more
-    const Cover c = cover(m.rows, (uint64_t)m.cols / (16 / mx_value_bytes(TYPE)) + 2, kGrid);
+    // a row that starts off a boundary may reach into one chunk more
+    const Cover c = cover(m.rows, mx_div_up((uint64_t)m.cols + 16 / mx_value_bytes(TYPE) - 1, kReadBack), kGrid);
     k_mx_dequantize_any<FMT, TYPE><<<c.grid, kThreads, 0, st>>>(m, out, stride_bytes, c);
   }
   return cudaGetLastError();
@@ -598,7 +610,7 @@ zipnn_status zipnn_mx_quantize(zipnn_mx_format format, zipnn_value_type type, co
   if (!mx_valid(format, rows, cols) || !mx_valid_type(type) || !x || !codes || !scales || off16(codes) || off16(scales))
     return ZIPNN_ERR_INVALID_ARG;
   const uint32_t B = mx_value_bytes(type);
-  if (reinterpret_cast<uintptr_t>(x) % B || row_stride < cols || row_stride > kMxMaxCols) return ZIPNN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(x) % B || row_stride < cols || row_stride > kMxMaxStride) return ZIPNN_ERR_INVALID_ARG;
   const bool find = format == ZIPNN_NVFP4 && find_global;
   if (format == ZIPNN_NVFP4 && (!global_scale || reinterpret_cast<uintptr_t>(global_scale) % 4)) return ZIPNN_ERR_INVALID_ARG;
   if (find && (!ws || off16(ws))) return ZIPNN_ERR_INVALID_ARG;
@@ -634,7 +646,7 @@ zipnn_status zipnn_mx_dequantize(zipnn_mx_format format, zipnn_value_type type, 
   if (!mx_valid(format, rows, cols) || !mx_valid_type(type) || !codes || !scales || !out || off16(codes) || off16(scales))
     return ZIPNN_ERR_INVALID_ARG;
   const uint32_t B = mx_value_bytes(type);
-  if (reinterpret_cast<uintptr_t>(out) % B || row_stride < cols || row_stride > kMxMaxCols) return ZIPNN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(out) % B || row_stride < cols || row_stride > kMxMaxStride) return ZIPNN_ERR_INVALID_ARG;
   if (format == ZIPNN_NVFP4 && (!global_scale || reinterpret_cast<uintptr_t>(global_scale) % 4)) return ZIPNN_ERR_INVALID_ARG;
   if (!device_ok()) return ZIPNN_ERR_UNSUPPORTED;
   const Packed m{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), global_scale, mx_row_bytes(cols),

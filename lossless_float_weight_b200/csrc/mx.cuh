@@ -17,9 +17,9 @@ __host__ __device__ constexpr uint64_t mx_col_tiles(int fmt, uint64_t cols) { re
 __host__ __device__ constexpr uint32_t mx_in_tile(uint32_t row, uint32_t block) {
   return 16 * (row % 32) + 4 * (row / 32 % 4) + block % 4;
 }
-// The largest sizes a call takes: every byte offset stays far inside 64 bits, and a row's
-// chunk index inside 32.
-constexpr uint64_t kMxMaxRows = 1ull << 31, kMxMaxCols = 1ull << 31;
+// The largest sizes a call takes: every byte offset stays far inside 64 bits, and a place in a
+// row inside an int.
+constexpr uint64_t kMxMaxRows = 1ull << 31, kMxMaxCols = 1ull << 30, kMxMaxStride = 1ull << 40;
 inline bool mx_valid(int fmt, uint64_t rows, uint64_t cols) {
   return (fmt == kMxFp4 || fmt == kNvFp4) && rows >= 1 && cols >= 1 && rows <= kMxMaxRows && cols <= kMxMaxCols;
 }

@@ -740,7 +740,7 @@ zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const 
                              uint64_t k, zipnn_value_type type, void* out, uint64_t row_stride, zipnn_stream_t stream) {
   if (!mx_valid(format, m, k) || !mx_valid(format, n, k) || !mx_valid_type(type)) return ZIPNN_ERR_INVALID_ARG;
   if (off16(a_codes) || off16(a_scales) || off16(b_codes) || off16(b_scales) || !out) return ZIPNN_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(out) % mx_value_bytes(type) || row_stride < n || row_stride > kMxMaxCols) return ZIPNN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(out) % mx_value_bytes(type) || row_stride < n || row_stride > kMxMaxStride) return ZIPNN_ERR_INVALID_ARG;
   if (format == ZIPNN_NVFP4 && (!a_global || !b_global || reinterpret_cast<uintptr_t>(a_global) % 4 || reinterpret_cast<uintptr_t>(b_global) % 4))
     return ZIPNN_ERR_INVALID_ARG;
   if (mx_div_up(m, 128) * mx_div_up(n, 128) > 0x7FFFFFFFull) return ZIPNN_ERR_INVALID_ARG;

@@ -92,8 +92,8 @@ class MxTensor:
             _fail("MxTensor: at least one dimension, the last not empty")
         self.cols = self.shape[-1]
         self.rows = self.shape[0] if len(self.shape) == 2 else _rows(self.shape)
-        if self.rows > 1 << 31 or self.cols > 1 << 31:
-            _fail("MxTensor: at most 2^31 rows and columns")
+        if self.rows > 1 << 31 or self.cols > 1 << 30:
+            _fail("MxTensor: at most 2^31 rows and 2^30 columns")
         if not (codes.is_cuda and codes.is_contiguous() and codes.element_size() == 1 and
                 codes.numel() == self.rows * _row_bytes(self.cols)):
             _fail("MxTensor: codes are rows x zipnn_mx_row_bytes(cols) contiguous CUDA bytes")
@@ -165,8 +165,8 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
             _fail("mx.quantize: global_scale is one FP32 value on x's device")
     elif global_scale is not None:
         _fail("mx.quantize: mxfp4 has no global_scale")
-    if rows > 1 << 31 or cols > 1 << 31:
-        _fail("mx.quantize: at most 2^31 rows and columns")
+    if rows > 1 << 31 or cols > 1 << 30:
+        _fail("mx.quantize: at most 2^31 rows and 2^30 columns")
     codes = torch.empty((rows, _row_bytes(cols)), dtype=torch.float4_e2m1fn_x2, device=dev)
     scales = torch.empty(_scale_bytes(format, rows, cols), dtype=_SCALE_DTYPES[format], device=dev)
     if rows:

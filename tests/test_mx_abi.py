@@ -20,7 +20,7 @@ def test_sizes(Z):
             blocks = -(-cols // blk)
             assert Z.zipnn_mx_scale_bytes(fmt, rows, cols) == -(-rows // 128) * -(-blocks // 4) * 512
         assert Z.zipnn_mx_scale_bytes(fmt, 0, 5) == 0 and Z.zipnn_mx_scale_bytes(fmt, 5, 0) == 0
-        assert Z.zipnn_mx_scale_bytes(fmt, (1 << 31) + 1, 5) == 0
+        assert Z.zipnn_mx_scale_bytes(fmt, (1 << 31) + 1, 5) == 0 and Z.zipnn_mx_scale_bytes(fmt, 5, (1 << 30) + 1) == 0
     assert Z.zipnn_mx_scale_bytes(2, 5, 5) == 0 and Z.zipnn_mx_row_bytes(0) == 0
 
 
@@ -33,7 +33,8 @@ def test_argument_errors_without_a_device(Z):
 
     for bad in (dict(fmt=2), dict(t=3), dict(x=None), dict(x=fake + 1), dict(t=Z.VALUE_FP32, x=fake + 2), dict(rows=0),
                 dict(cols=0, stride=0), dict(stride=63), dict(g=None), dict(g=fake + 2), dict(codes=None),
-                dict(codes=fake + 8), dict(scales=fake + 4), dict(w=None), dict(w=fake + 4), dict(rows=(1 << 31) + 1)):
+                dict(codes=fake + 8), dict(scales=fake + 4), dict(w=None), dict(w=fake + 4), dict(rows=(1 << 31) + 1),
+                dict(cols=(1 << 30) + 1, stride=(1 << 30) + 1), dict(stride=(1 << 40) + 1)):
         assert quant(**bad) == Z.ERR_INVALID_ARG, bad
     assert quant(wb=ws - 1) == Z.ERR_OUT_TOO_SMALL
 
@@ -49,7 +50,7 @@ def test_argument_errors_without_a_device(Z):
 
     for bad in (dict(fmt=2), dict(ac=None), dict(asc=fake + 8), dict(ag=None), dict(bc=fake + 4), dict(bsc=None), dict(bg=fake + 1),
                 dict(m=0), dict(n=0), dict(k=0), dict(t=5), dict(out=None), dict(out=fake + 1), dict(stride=7),
-                dict(m=1 << 31, n=1 << 31, stride=1 << 31)):
+                dict(m=1 << 31, n=1 << 31, stride=1 << 31), dict(stride=(1 << 40) + 1)):
         assert matmul(**bad) == Z.ERR_INVALID_ARG, bad
     if not torch.cuda.is_available():
         assert matmul() == Z.ERR_UNSUPPORTED and matmul(fmt=Z.MXFP4, ag=None, bg=None) == Z.ERR_UNSUPPORTED
