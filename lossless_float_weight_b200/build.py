@@ -10,7 +10,8 @@ LIB = os.path.join(HERE, "libzipnn_b200.so")
 SOURCES = ["api.cu", "prelude.cu", "decode.cu", "plan.cu", "timing.cu", "noalloc.cu", "encode_bf16.cu", "encode_fp32.cu",
            "encode_sub.cu", "shard.cu", "pack.cu", "mx.cu",
            "mx_matmul.cu", "pages.cu"]
-HEADERS = ["bulk.cuh", "common.cuh", "fields.cuh", "huffman.cuh", "launch.h", "mx.cuh"]
+HEADERS = ["bulk.cuh", "common.cuh", "fields.cuh", "huffman.cuh", "launch.h", "mx.cuh",
+           "op_ids.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CSRC,

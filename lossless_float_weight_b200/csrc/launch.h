@@ -10,8 +10,7 @@ namespace zipnn {
 bool device_ok();
 
 // Kernel ids of the optional event timing (timing.cu).
-enum KernelId { kIdHist = 0, kIdBuild, kIdLayout, kIdEncode, kIdDecode, kIdCodeLengths, kIdPlan, kIdShard, kIdPackHist, kIdPackEncode, kIdMxAmax,
-                kIdMxQuantize, kIdMxDequantize, kIdMxMatmul, kIdPagesPlan, kIdPagesMove, kNumKernelIds };
+enum KernelId { kIdHist = 0, kIdBuild, kIdLayout, kIdEncode, kIdDecode, kIdCodeLengths, kIdPlan, kIdShard, kIdPackHist, kIdPackEncode, kNumKernelIds };
 
 // Brackets one launch with CUDA events on `st` while timing is enabled.
 class TimedLaunch {

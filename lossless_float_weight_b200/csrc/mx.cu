@@ -7,8 +7,8 @@
 
 #include "zipnn.h"
 #include "common.cuh"
-#include "launch.h"
 #include "mx.cuh"
+#include "op_ids.h"
 
 namespace zipnn {
 namespace {

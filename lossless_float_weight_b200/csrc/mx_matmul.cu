@@ -16,8 +16,8 @@
 #include "zipnn.h"
 #include "bulk.cuh"
 #include "common.cuh"
-#include "launch.h"
 #include "mx.cuh"
+#include "op_ids.h"
 
 namespace zipnn {
 namespace {
@@ -667,7 +667,7 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, uint64_t cols, Args
   at[0].val.clusterDim.x = a.split;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.split > 1;
   TimedLaunch t(kIdMxMatmul, st);
   return cudaLaunchKernelEx(&cfg, k_mx_matmul<FMT, BN>, pm, qm, a);
 }

@@ -9,7 +9,7 @@
 
 #include "zipnn.h"
 #include "common.cuh"
-#include "launch.h"
+#include "op_ids.h"
 
 namespace zipnn {
 namespace {

@@ -5,12 +5,12 @@
 #include <vector>
 
 #include "zipnn.h"
-#include "launch.h"
+#include "op_ids.h"
 
 namespace zipnn {
 namespace {
 
-const char* const kNames[kNumKernelIds] = {"split_hist", "code_build", "layout_scan", "encode",
+const char* const kNames[kNumAllIds] = {"split_hist", "code_build", "layout_scan", "encode",
                                            "decode_merge", "code_lengths", "plan", "shard_tables",
                                            "pack_hist", "pack_encode", "mx_amax", "mx_quantize", "mx_dequantize", "mx_matmul",
                                            "pages_plan", "pages_move"};
@@ -25,8 +25,8 @@ struct Timing {
   bool enabled = false;
   std::vector<cudaEvent_t> pool;
   std::vector<Pending> pending;
-  double ms[kNumKernelIds] = {0};
-  uint64_t launches[kNumKernelIds] = {0};
+  double ms[kNumAllIds] = {0};
+  uint64_t launches[kNumAllIds] = {0};
 };
 
 Timing& timing() {
@@ -93,19 +93,19 @@ zipnn_status zipnn_timing_collect(double* ms, uint64_t* launches, uint32_t count
     t.pool.push_back(p.stop);
   }
   t.pending.clear();
-  for (uint32_t i = 0; i < count && i < (uint32_t)kNumKernelIds; i++) {
+  for (uint32_t i = 0; i < count && i < (uint32_t)kNumAllIds; i++) {
     if (ms) ms[i] = t.ms[i];
     if (launches) launches[i] = t.launches[i];
   }
-  for (int i = 0; i < kNumKernelIds; i++) {
+  for (int i = 0; i < kNumAllIds; i++) {
     t.ms[i] = 0;
     t.launches[i] = 0;
   }
   return st;
 }
 
-uint32_t zipnn_kernel_count(void) { return (uint32_t)kNumKernelIds; }
+uint32_t zipnn_kernel_count(void) { return (uint32_t)kNumAllIds; }
 
-const char* zipnn_kernel_name(uint32_t id) { return id < (uint32_t)kNumKernelIds ? kNames[id] : "unknown"; }
+const char* zipnn_kernel_name(uint32_t id) { return id < (uint32_t)kNumAllIds ? kNames[id] : "unknown"; }
 
 }  // extern "C"

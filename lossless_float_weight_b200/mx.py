@@ -13,7 +13,8 @@ quantised weight or K/V cache goes through :func:`compress` and comes back bit f
 
 The functions check their arguments, allocate with PyTorch and call the CUDA library on
 the current stream of the tensors' device (or `stream`); they do not synchronise, except
-:func:`compress` and :func:`decompress`, as the codec's own.
+:func:`compress` and :func:`decompress`, as the codec's own. They are for stored and served
+tensors: no gradient passes through them, and an input that asks for one is refused.
 """
 import torch
 
@@ -149,6 +150,8 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
     f, type = _format(format), _VALUES.get(x.dtype)
     if type is None or not x.is_cuda or x.dim() == 0 or x.shape[-1] == 0:
         _fail("mx.quantize: a CUDA tensor (..., K) of BF16, FP16 or FP32")
+    if x.requires_grad and torch.is_grad_enabled():
+        _fail("mx.quantize: no gradient passes through it; detach x or use torch.no_grad()")
     shape, dev = tuple(x.shape), x.device
     cols = shape[-1]
     m = x if len(shape) == 2 else x.reshape(-1, cols)

@@ -157,9 +157,9 @@ def test_other_stream_and_graph(mx):
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    for handle in (s, s.cuda_stream):
+    for handle in (s, s.cuda_stream, 0, torch.cuda.default_stream()):
         got = [mx.dequantize(mx.quantize(x, f, stream=handle), torch.float32, stream=handle) for f in ("mxfp4", "nvfp4")]
-        s.synchronize()
+        torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     g, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
     xs, ys = x.clone(), x.clone()
@@ -221,7 +221,7 @@ def test_refusals_on_the_device(mx):
     one = torch.ones(1, device="cuda")
     for call in (lambda: mx.quantize(x, "mxfp4", one), lambda: mx.quantize(x, "nvfp4", one.double()),
                  lambda: mx.quantize(x, "nvfp4", torch.ones(2, device="cuda")), lambda: mx.quantize(x, "nvfp4", torch.ones(1)),
-                 lambda: mx.quantize(x[:, :0]), lambda: mx.quantize(x[0, 0]), lambda: mx.dequantize(q, torch.float64),
+                 lambda: mx.quantize(x[:, :0]), lambda: mx.quantize(x.clone().requires_grad_()), lambda: mx.quantize(x[0, 0]), lambda: mx.dequantize(q, torch.float64),
                  lambda: mx.dequantize(q, torch.bfloat16, out=torch.empty(4, 64, device="cuda")),
                  lambda: mx.dequantize(q, torch.float32, out=torch.empty(64, 4, device="cuda").t()),
                  lambda: mx.MxTensor(q.codes, q.scales, (4, 64), "nvfp4"),

@@ -102,7 +102,29 @@ def test_leading_dimensions_plain_activations_and_empty(mx):
         assert torch.equal(y, mx.matmul(mx.quantize(x, fmt), b))
         assert torch.equal(y.view(10, 200), mx.matmul(x.view(10, 96), b))
         assert mx.matmul(x[:0], b).shape == (0, 5, 200)
+        assert torch.equal(mx.matmul(x[1, 2], b), mx.matmul(x[1, 2:3], b)[0])
         assert mx.matmul(x, mx.quantize(w[:0], fmt)).shape == (2, 5, 0)
+
+
+@pytest.mark.parametrize("m,n", [(66_000, 33_000), (40, 70_000_000)])
+def test_an_output_past_32_bits(mx, m, n):
+    """2.2 and 2.8 billion results: some rows and columns of each end against the 64-bit product."""
+    k = 64
+    a, va = random_mx(mx, m, k, "mxfp4", 1, exact=True)
+    if n < 100_000:
+        b, vb = random_mx(mx, n, k, "mxfp4", 2, exact=True)
+    else:  # the same rows again and again
+        b, vb = random_mx(mx, 1 << 12, k, "mxfp4", 2, exact=True)
+        reps = -(-n // (1 << 12))
+        rows = reps << 12
+        b = mx.MxTensor(b.codes.repeat(reps, 1)[:n].contiguous(),
+                        b.scales.view(torch.uint8).repeat(reps)[: -(-n // 128) * 512].contiguous(), (n, k), "mxfp4")
+        assert rows >= n
+    y = mx.matmul(a, b, torch.bfloat16)
+    i, j = np.r_[0:3, m // 2, m - 3:m], np.r_[0:3, n // 2, n - 3:n]
+    got = y[torch.from_numpy(i).cuda()][:, torch.from_numpy(j).cuda()].double().cpu().numpy()
+    want = va[i] @ vb[j % vb.shape[0]].T
+    assert np.array_equal(got, torch.from_numpy(want).to(torch.bfloat16).double().numpy())
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
