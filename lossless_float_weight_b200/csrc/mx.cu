@@ -181,6 +181,20 @@ __device__ __forceinline__ uint32_t top_bits(uint32_t t) {
   return __float_as_uint(__half2float(__ushort_as_half((unsigned short)t)));
 }
 
+// n values times `by`, two to an instruction.
+template <int N>
+__device__ __forceinline__ void times(const float* v, float by, float* q) {
+  uint64_t b;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(b) : "f"(by));
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    uint64_t x, y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(v[i]), "f"(v[i + 1]));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(b));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(q[i]), "=f"(q[i + 1]) : "l"(y));
+  }
+}
+
 // Two FP32 quotients to a byte of two E2M1 codes (the first in the low nibble), four such
 // bytes: the type's own rounding, ties to even, saturating.
 __device__ __forceinline__ uint32_t to_e2m1(const float* q) {
@@ -264,12 +278,11 @@ __device__ __forceinline__ void nv_codes(const uint32_t (&w)[kWords<TYPE>], int 
   const float below = inv * (1.f - 0x1p-21f), above = inv * (1.f + 0x1p-21f);
   uint32_t other[2];
   {
-    float q[16], r[16];
+    float x[16], q[16], r[16];
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const float x = value_of<TYPE>(w, from + i);
-      q[i] = x * below, r[i] = x * above;
-    }
+    for (int i = 0; i < 16; i++) x[i] = value_of<TYPE>(w, from + i);
+    times<16>(x, below, q);
+    times<16>(x, above, r);
     codes[0] = to_e2m1(q), codes[1] = to_e2m1(q + 8);
     other[0] = to_e2m1(r), other[1] = to_e2m1(r + 8);
   }
@@ -376,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, FMT == kNvFp4 ? 3 : 4) k_mx_quantize
         const float inv = __uint_as_float((254 - byte) << 23);  // 2^(127 - byte), a normal number
         float q[32];
 #pragma unroll
-        for (int i = 0; i < 32; i++) q[i] = value_of<TYPE>(w, i) * inv;  // exact where it matters: above 2^-126
+        for (int i = 0; i < 32; i++) q[i] = value_of<TYPE>(w, i);
+        times<32>(q, inv, q);  // exact where it matters: above 2^-126
 #pragma unroll
         for (int i = 0; i < 4; i++) out[i] = to_e2m1(q + 8 * i);
       }
