@@ -40,31 +40,35 @@ struct Args {
   uint32_t stages, mmas;       // of the whole row
   uint32_t split;              // blocks of a cluster, each a range of the stages
   uint32_t depth, tmem_cols;
-  int type, p_is_n, pairs;
+  int type, p_is_n;
 };
+
+constexpr uint32_t kSmallest = 80 * 1024;  // below the shared memory of every block here
 
 template <int FMT, int BN>
 struct Shape {
   static constexpr uint32_t kTiles = kStageK / (4 * mx_block(FMT));  // scale tiles of a stage along a row: 2 or 4
-  static constexpr uint32_t kHalves = BN > 128 ? 2 : 1;               // row tiles of Q's scales
-  static constexpr uint32_t kP = 128 * kStageBytesK, kQ = BN * kStageBytesK;
-  static constexpr uint32_t kSp = kTiles * kMxTileBytes, kSq = kSp * kHalves;
-  static constexpr uint32_t kStage = (kP + kQ + kSp + kSq + 1023) / 1024 * 1024;
+  static constexpr uint32_t kP = 128 * kStageBytesK, kQ = BN * kStageBytesK, kScales = kTiles * kMxTileBytes;
+  static constexpr uint32_t kStage = (kP + kQ + 2 * kScales + 1023) / 1024 * 1024;
   // Stages in flight. Where the grid has more blocks than the device has SMs, two share one
   // (100 x 32000 x 4096: 17.2 us, and 20.3 us with one block and its deeper ring); else a
   // block has the SM's shared memory to itself (128 x 11008 x 4096: 9.6 us, and 10.8 with 3).
-  static constexpr uint32_t kShared = BN <= 64 ? 4 : 3, kAlone = BN <= 64 ? 6 : 5;
+  static constexpr uint32_t kHalf = (113 * 1024 - 1280) / kStage, kShared = kHalf < 4 ? kHalf : 4, kAlone = BN <= 64 ? 6 : 5;
   static constexpr uint32_t smem(uint32_t depth) { return depth * kStage + 1024 + 256; }
+  static_assert(kShared * kStage >= kSmallest, "the smallest block");
   // Tensor memory: the sums, and a set of scales for each stage in shared memory (4 columns a
   // tile), so that a set is written again only after the instructions that read it are done:
   // the stage's codes were not brought before that either.
-  static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kHalves);
+  static constexpr uint32_t kScaleCols = 2 * 4 * kTiles;
   static constexpr uint32_t cols(uint32_t depth) {
     const uint32_t used = BN + depth * kScaleCols;
     return used <= 64 ? 64 : used <= 128 ? 128 : used <= 256 ? 256 : 512;
   }
   static_assert(smem(kAlone) <= 227 * 1024 && BN + kAlone * kScaleCols <= 512, "one block to an SM");
-  static_assert(2 * cols(kShared) <= 512, "two blocks to an SM");
+  // Two blocks on an SM, of one call or of two, never wait for each other's tensor memory
+  // (which could close a ring of clusters): a block that leaves room for another one's shared
+  // memory takes at most half of it.
+  static_assert(cols(kShared) <= 256 && (cols(kAlone) <= 256 || smem(kAlone) + kSmallest > 227 * 1024), "tensor memory");
 };
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -239,17 +243,15 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   // Stage i of the row into place `at` of the ring. Scale tiles that the row does not have are
   // not brought.
   const auto bring = [&](uint32_t i, uint32_t at) {
-    const uint32_t halves = S::kHalves == 2 && q0 + 128 < a.q_rows ? 2 : 1;
     uint8_t* st = smem + at * S::kStage;
     uint64_t* bar = full + at;
     const uint32_t t0 = i * S::kTiles, bytes = min(S::kTiles, a.col_tiles - t0) * kMxTileBytes;
-    mbar_expect_tx(bar, S::kP + S::kQ + bytes * (1 + halves));
+    mbar_expect_tx(bar, S::kP + S::kQ + 2 * bytes);
     tma_2d(st, &p_map, (int32_t)(i * kStageBytesK), (int32_t)p0, bar);
     tma_2d(st + S::kP, &q_map, (int32_t)(i * kStageBytesK), (int32_t)q0, bar);
     uint8_t* sc = st + S::kP + S::kQ;
     bulk_g2s(sc, a.p_scales + ((uint64_t)(p0 / 128) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
-    for (uint32_t h = 0; h < halves; h++)
-      bulk_g2s(sc + S::kSp + h * S::kSp, a.q_scales + ((uint64_t)(q0 / 128 + h) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
+    bulk_g2s(sc + S::kScales, a.q_scales + ((uint64_t)(q0 / 128) * a.col_tiles + t0) * kMxTileBytes, bytes, bar);
   };
   const uint32_t early = min(hi - lo, a.depth);  // stages brought before the block has met
   if (warp == 4) {
@@ -303,16 +305,14 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
 #pragma unroll
         for (uint32_t t = 0; t < S::kTiles; t++) {
           copy_scales(tp + 4 * t, sc + t * kMxTileBytes);
-#pragma unroll
-          for (uint32_t h = 0; h < S::kHalves; h++)
-            copy_scales(tq + 4 * (t * S::kHalves + h), sc + S::kSp + h * S::kSp + t * kMxTileBytes);
+          copy_scales(tq + 4 * t, sc + S::kScales + t * kMxTileBytes);
         }
 #pragma unroll
         for (uint32_t k = 0; k < kStageK / kMmaK; k++) {
           if (k >= left) break;
           const uint32_t t = FMT == kMxFp4 ? k / 2 : k, id = FMT == kMxFp4 ? k % 2 * 2 : 0;
           mma<FMT>(tmem, desc_codes(st + k * 32), desc_codes(st + S::kP + k * 32), instr<FMT, BN>(id), tp + 4 * t,
-                   tq + 4 * t * S::kHalves, i + k > lo);
+                   tq + 4 * t, i + k > lo);
         }
         commit(empty + r.at);
       }
@@ -373,15 +373,16 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
 // ---- Two blocks to a tile --------------------------------------------------------------
 // Large products are bound by what the codes' tiles cost between L2 and shared memory: a stage
 // of a 128 x 128 tile brings 34 KB for 256 cycles of the tensor cores. Here the two blocks of a
-// cluster compute 256 x BN together (cta_group::2): each brings its own 128 rows of P and half
+// cluster compute 256 x 256 together (cta_group::2): each brings its own 128 rows of P and half
 // of the rows of Q, and both read both halves. One thread of the first block issues the
 // instructions for both, and the sums of a tile leave tensor memory through the registers of
 // eight warps, whose stores overlap with the next tile's instructions. Blocks walk over the
 // tiles, one pair on two SMs.
-constexpr int kPairThreads = 320;
+constexpr int kPairThreads = 320, kPairCols = 256;
 
-template <int FMT, int BN>
+template <int FMT>
 struct PairShape {
+  static constexpr int BN = kPairCols;
   static constexpr uint32_t kTiles = kStageK / (4 * mx_block(FMT));
   static constexpr uint32_t kHalves = BN / 128;  // row tiles of Q's scales: every block needs all of them
   static constexpr uint32_t kP = 128 * kStageBytesK, kQ = BN / 2 * kStageBytesK;
@@ -392,6 +393,7 @@ struct PairShape {
   static constexpr uint32_t kFit = (227 * 1024 - 1024 - 512) / kStage, kRoom = (512 - BN) / kScaleCols;
   static constexpr uint32_t kDepth = kFit < kRoom ? kFit : kRoom;
   static constexpr uint32_t kSmem = kDepth * kStage + 1024 + 512;
+  static_assert(kSmem + kSmallest > 227 * 1024, "all of the tensor memory, so no other block on the SM");
 };
 
 __device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
@@ -449,9 +451,10 @@ struct PairMaps {
   CUtensorMap p, q, sp, sq;
 };
 
-template <int FMT, int BN>
+template <int FMT>
 __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid_constant__ PairMaps maps, const Args a) {
-  using S = PairShape<FMT, BN>;
+  using S = PairShape<FMT>;
+  constexpr int BN = kPairCols;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kDepth * S::kStage);
@@ -682,15 +685,16 @@ bool scale_map(CUtensorMap* m, const uint8_t* scales, uint64_t row_tiles, uint64
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int BN>
+template <int FMT>
 cudaError_t launch_pairs(const Operand& p, const Operand& q, uint64_t cols, Args a, cudaStream_t st) {
-  using S = PairShape<FMT, BN>;
+  using S = PairShape<FMT>;
+  constexpr int BN = kPairCols;
   static std::atomic<uint64_t> ready{0};
   int dev = 0, sms = 0;
   cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_mx_matmul_pair<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    e = cudaFuncSetAttribute(k_mx_matmul_pair<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -714,12 +718,12 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, uint64_t cols, Args
   cfg.attrs = at;
   cfg.numAttrs = 1;
   TimedLaunch t(kIdMxMatmul, st);
-  return cudaLaunchKernelEx(&cfg, k_mx_matmul_pair<FMT, BN>, maps, a);
+  return cudaLaunchKernelEx(&cfg, k_mx_matmul_pair<FMT>, maps, a);
 }
 
 template <int FMT>
-cudaError_t launch_matmul(const Operand& p, const Operand& q, uint64_t cols, const Args& a, cudaStream_t st) {
-  if (a.pairs) return launch_pairs<FMT, 256>(p, q, cols, a, st);
+cudaError_t launch_matmul(bool pairs, const Operand& p, const Operand& q, uint64_t cols, const Args& a, cudaStream_t st) {
+  if (pairs) return launch_pairs<FMT>(p, q, cols, a, st);
   if (q.rows <= 16) return launch_tiles<FMT, 16>(p, q, cols, a, st);
   if (q.rows <= 32) return launch_tiles<FMT, 32>(p, q, cols, a, st);
   if (q.rows <= 64) return launch_tiles<FMT, 64>(p, q, cols, a, st);
@@ -767,9 +771,8 @@ zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const 
   g.mmas = (uint32_t)mx_div_up(k, kMmaK);
   g.type = type;
   g.p_is_n = p_is_n;
-  g.pairs = pairs;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = format == ZIPNN_MXFP4 ? launch_matmul<kMxFp4>(p, q, k, g, st) : launch_matmul<kNvFp4>(p, q, k, g, st);
+  const cudaError_t e = format == ZIPNN_MXFP4 ? launch_matmul<kMxFp4>(pairs, p, q, k, g, st) : launch_matmul<kNvFp4>(pairs, p, q, k, g, st);
   return e == cudaSuccess ? ZIPNN_OK : ZIPNN_ERR_CUDA;
 }
 

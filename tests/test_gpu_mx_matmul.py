@@ -162,6 +162,23 @@ def test_same_bits_each_time_two_streams_and_graphs(mx):
     assert mx.status() == Z.OK
 
 
+def test_every_kind_of_block_at_once(mx):
+    """Products of all the kernels' shapes side by side on six streams, again and again: equal
+    bits each time, whatever shares an SM with whatever."""
+    sizes = [(1, 4096, 2048, "nvfp4"), (17, 3000, 1024, "nvfp4"), (64, 2000, 4096, "mxfp4"), (128, 4096, 2048, "nvfp4"),
+             (1700, 1600, 512, "mxfp4"), (1537, 2049, 640, "nvfp4"), (100, 20000, 512, "mxfp4"), (9, 128, 11008, "mxfp4")]
+    ab = [(random_mx(mx, m, k, f, 1)[0], random_mx(mx, n, k, f, 2)[0]) for m, n, k, f in sizes]
+    want = [mx.matmul(a, b) for a, b in ab]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    for turn in range(10):
+        got = [mx.matmul(a, b, stream=streams[(i + turn) % 6]) for i, (a, b) in enumerate(ab) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[3 * i + j], want[i]) for i in range(len(ab)) for j in range(3))
+    from lossless_float_weight_b200 import zipnn as Z
+    assert mx.status() == Z.OK
+
+
 def test_weights_through_the_codec(mx):
     """A weight quantised, compressed, decompressed and multiplied, as a stored model is used."""
     g = torch.Generator().manual_seed(4)
