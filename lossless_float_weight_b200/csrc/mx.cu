@@ -1,7 +1,10 @@
 // mx.cu -- microscaled 4-bit matrices (include/zipnn.h): quantisation and reading back.
 //
 // Both are one pass over the data with a few operations a value, so HBM bounds them: BF16 to
-// MXFP4 moves 2 + 0.5 + 1/32 bytes a value each way.
+// MXFP4 moves 2 + 0.5 + 1/32 bytes a value each way. Measured on 11008 x 4096 BF16 (114 MB in
+// all): MXFP4 19 us (6.0 TB/s), NVFP4 with a given scale 25 us (its border tests: 17 M warp
+// instructions, MXFP4's 9 M), with its scale found 42 us (amax reads x once more, 17.5 us);
+// read back 21.5 us (5.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -590,6 +593,7 @@ cudaError_t launch_quantize(const Matrix& m, float* global_scale, bool find, uin
 template <int FMT, int TYPE>
 cudaError_t launch_dequantize(const Packed& m, uint8_t* out, uint64_t stride_bytes, cudaStream_t st) {
   TimedLaunch t(kIdMxDequantize, st);
+  // 11008 x 4096 to BF16 takes 21.5 us by the one, 11008 x 4097 34 us by the other
   if (reinterpret_cast<uintptr_t>(out) % 32 == 0 && stride_bytes % 32 == 0) {
     const Cover c = cover(m.rows, mx_div_up(m.cols, kReadBack), kGrid);
     k_mx_dequantize<FMT, TYPE><<<c.grid, kThreads, 0, st>>>(m, out, stride_bytes, c);
@@ -639,6 +643,7 @@ zipnn_status zipnn_mx_quantize(zipnn_mx_format format, zipnn_value_type type, co
   uint8_t *c = static_cast<uint8_t*>(codes), *s = static_cast<uint8_t*>(scales);
   uint32_t* p = static_cast<uint32_t*>(ws);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // 11008 x 4096 BF16 to MXFP4 takes 19 us by the one, 11008 x 4097 23 us by the other
   const bool even = reinterpret_cast<uintptr_t>(x) % 32 == 0 && m.stride_bytes % 32 == 0;
 #define ZIPNN_MX_CASE(F, T)                                                                          \
   if (format == F && type == T)                                                                      \

@@ -5,6 +5,8 @@
 // The data is moved once (read and written, nothing else), so HBM bounds the large calls; the
 // small ones are bound by launches, and take one or two: a single block decides what the
 // call does, and a grid that starts beside it (programmatic dependent launch) does it.
+// Measured (32 KB pages, 64 planes): 640 pages scattered 390 us (6.9 TB/s), 174 pages closed up
+// 122 us (6.0 TB/s), 5 pages gathered 4.4 us, a fork of one sequence 7 us, a free 2.5 us.
 #include <algorithm>
 
 #include "zipnn.h"
