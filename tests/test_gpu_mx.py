@@ -194,6 +194,36 @@ def test_a_matrix_past_32_bits(mx):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_rows_longer_than_the_grid(mx, fmt):
+    """More columns than the blocks beside each other cover in the pass for the largest value
+    (1024 blocks of 8192): the largest is the last."""
+    x = make(1, 9_000_011, "fp32", 3)
+    x[0, -1] = 50000.0
+    check_quantize(mx, x, fmt)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 33), (129, 47), (5, 4097), (128, 64)])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_nothing_written_past_codes_scales_and_scale(mx, fmt, rows, cols):
+    from lossless_float_weight_b200 import zipnn as Z
+    f = {"mxfp4": Z.MXFP4, "nvfp4": Z.NVFP4}[fmt]
+    x = make(rows, cols, "bf16", 1).cuda()
+    nc, ns = rows * Z.zipnn_mx_row_bytes(cols), Z.zipnn_mx_scale_bytes(f, rows, cols)
+    codes, scales = (torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda") for n in (nc, ns))
+    g = torch.full((9,), 7.0, device="cuda")
+    ws = torch.full((Z.MX_WORKSPACE_BYTES + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    assert Z.zipnn_mx_quantize(f, Z.VALUE_BF16, x.data_ptr(), rows, cols, cols, g[4:].data_ptr(), 1, codes[256:].data_ptr(),
+                               scales[256:].data_ptr(), ws.data_ptr(), Z.MX_WORKSPACE_BYTES, s) == Z.OK
+    q = mx.quantize(x, fmt)
+    for buf, n, want in ((codes, nc, q.codes), (scales, ns, q.scales)):
+        assert torch.equal(buf[256:256 + n], want.view(torch.uint8).reshape(-1))
+        assert (buf[:256] == 0xA5).all() and (buf[256 + n:] == 0xA5).all()
+    assert (ws[Z.MX_WORKSPACE_BYTES:] == 0x5A).all()
+    assert (g[:4] == 7).all() and (g[5:] == 7).all() and (fmt == "mxfp4" or g[4] == q.global_scale[0])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_through_the_codec(mx, fmt):
     x = make(300, 500, "bf16", 12).cuda()
     q = mx.quantize(x, fmt)
