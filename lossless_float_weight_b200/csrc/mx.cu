@@ -2,9 +2,9 @@
 //
 // Both are one pass over the data with a few operations a value, so HBM bounds them: BF16 to
 // MXFP4 moves 2 + 0.5 + 1/32 bytes a value each way. Measured on 11008 x 4096 BF16 (114 MB in
-// all): MXFP4 19 us (6.0 TB/s), NVFP4 with a given scale 25 us (its border tests: 17 M warp
-// instructions, MXFP4's 9 M), with its scale found 42 us (amax reads x once more, 17.5 us);
-// read back 21.5 us (5.4 TB/s).
+// all): MXFP4 19 us (6.0 TB/s), NVFP4 with a given scale 25 us (its border tests: 13 M warp
+// instructions, MXFP4's 8 M), with its scale found 43 us (amax reads x once more, 17.5 us);
+// read back 20.5 us (5.6 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -211,10 +211,11 @@ __device__ __forceinline__ uint32_t to_e2m1(const float* q) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t to_e4m3(float x) {
+// Two values to E4M3, to the nearest (ties to even), at most 448: the first in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3(float x, float y) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
-  return r & 0xFF;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  return r;
 }
 __device__ __forceinline__ float from_e4m3(uint32_t b) {
   uint32_t h2;
@@ -223,19 +224,30 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
   return __half2float(__ushort_as_half((unsigned short)h2));
 }
 
-// The E4M3 code nearest to amax / (6 g). The FP32 quotient is off by less than 4 of its last
-// steps; where a border between two codes is nearer than that, or the quotient leaves the
-// range where the borders have at most 4 bits, it is taken again in 64 bits and rounded to
-// odd in FP32 (23 bits and a sticky one hold every border apart).
+// What quotients are taken with, so that one is below the exact one and one above it: FP32
+// factors and products are off by less than 2^-22 here.
+constexpr float kBelow = 1.f - 0x1p-21f, kAbove = 1.f + 0x1p-21f;
+
+// Where 1 / g and what is done with it below are ordinary numbers.
+__device__ __forceinline__ bool usual(float g) { return g >= 1e-30f && g <= 1e30f; }
+
+// The E4M3 code nearest to amax / (6 g). Where the quotients from below and above round
+// apart, the sign of amax - m 6 g decides, m their border: m 6 has 7 bits, and the fused
+// product rounds once, so the sign is exact.
 __device__ __forceinline__ uint32_t nv_scale(float amax, float g, float inv6g) {
-  float t = amax * inv6g;
-  const uint32_t low = (__float_as_uint(t) + 8) & 0x7FFFF;
-  if (low < 16 || !(t >= 0.0156250f && t <= 1e30f)) {
+  if (!usual(g)) {
+    // the quotient in 64 bits, rounded to odd in FP32 (23 bits and a sticky one hold every
+    // border apart)
     const double want = (double)amax / (6.0 * (double)g);
-    t = __double2float_rz(want);
+    float t = __double2float_rz(want);
     if ((double)t != want) t = __uint_as_float(__float_as_uint(t) | 1u);
+    return to_e4m3(t, 0.f) & 0xFF;
   }
-  return to_e4m3(t);
+  const float t = amax * inv6g;
+  const uint32_t both = to_e4m3(t * kBelow, t * kAbove), low = both & 0xFF, high = both >> 8;
+  if (low == high) return low;
+  const float m = 0.5f * (from_e4m3(low) + from_e4m3(high)), d = fmaf(-6.f * m, g, amax);
+  return d > 0.f || (d == 0.f && (low & 1)) ? high : low;
 }
 
 // The codes of 16 values for a unit s g out of the range of nv_codes: |x| against the seven
@@ -278,7 +290,7 @@ __device__ __forceinline__ void nv_codes(const uint32_t (&w)[kWords<TYPE>], int 
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(u));
   if (s == 0.f) inv = 0.f;
-  const float below = inv * (1.f - 0x1p-21f), above = inv * (1.f + 0x1p-21f);
+  const float below = inv * kBelow, above = inv * kAbove;
   uint32_t other[2];
   {
     float x[16], q[16], r[16];
@@ -568,7 +580,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize_any(Packed m, uint8_
   }
 }
 
-constexpr uint32_t kGrid = 148 * 8;  // every thread of the device at 256 a block
+constexpr uint32_t kGrid = 148 * 8;       // every thread of the device at 256 a block
+constexpr uint32_t kReadGrid = 148 * 32;  // 11008 x 4096 read back: 20.5 us, 21.7 with kGrid; 11008 x 4097 30 and 34
 
 template <int FMT, int TYPE, bool ALIGNED>
 cudaError_t launch_quantize(const Matrix& m, float* global_scale, bool find, uint8_t* codes, uint8_t* scales,
@@ -595,11 +608,11 @@ cudaError_t launch_dequantize(const Packed& m, uint8_t* out, uint64_t stride_byt
   TimedLaunch t(kIdMxDequantize, st);
   // 11008 x 4096 to BF16 takes 21.5 us by the one, 11008 x 4097 34 us by the other
   if (reinterpret_cast<uintptr_t>(out) % 32 == 0 && stride_bytes % 32 == 0) {
-    const Cover c = cover(m.rows, mx_div_up(m.cols, kReadBack), kGrid);
+    const Cover c = cover(m.rows, mx_div_up(m.cols, kReadBack), kReadGrid);
     k_mx_dequantize<FMT, TYPE><<<c.grid, kThreads, 0, st>>>(m, out, stride_bytes, c);
   } else {
     // a row that starts off a boundary may reach into one chunk more
-    const Cover c = cover(m.rows, mx_div_up((uint64_t)m.cols + 16 / mx_value_bytes(TYPE) - 1, kReadBack), kGrid);
+    const Cover c = cover(m.rows, mx_div_up((uint64_t)m.cols + 16 / mx_value_bytes(TYPE) - 1, kReadBack), kReadGrid);
     k_mx_dequantize_any<FMT, TYPE><<<c.grid, kThreads, 0, st>>>(m, out, stride_bytes, c);
   }
   return cudaGetLastError();
