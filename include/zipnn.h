@@ -400,7 +400,8 @@ size_t zipnn_pages_workspace_bytes(uint32_t seqs, uint32_t pages);
  * skips the pair). src and dst are the same pool, or do not overlap. Refused with
  * ZIPNN_ERR_INVALID_ARG in the status, and then nothing copied: a destination named twice,
  * and within one pool a destination that is also a source. A number past the pool's pages
- * gives the same status; with dst_ids NULL the other pairs are then copied all the same. */
+ * gives the same status; from another pool with dst_ids NULL (where nothing else can go
+ * wrong) the other pairs are copied all the same. */
 zipnn_status zipnn_pages_copy(const zipnn_page_pool* src, const int32_t* src_ids, const zipnn_page_pool* dst,
                               const int32_t* dst_ids, uint32_t count, uint64_t page_bytes, void* ws, size_t ws_bytes,
                               zipnn_stream_t stream);

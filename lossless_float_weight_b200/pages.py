@@ -22,9 +22,13 @@ import torch
 from . import zipnn as Z
 from .mx import _call, _fail, _use
 
-# types of the codec, and the ones it stores by their bits
-_CODEC = {torch.float16: torch.bfloat16, torch.uint8: torch.float8_e4m3fn, torch.int8: torch.float8_e4m3fn,
-          torch.float8_e5m2: torch.float8_e4m3fn, torch.int16: torch.bfloat16}
+
+def _codec_dtype(dtype, what):
+    """The codec's type that stores a dtype by its bits."""
+    if dtype in Z._TORCH_DTYPES:
+        return dtype
+    return {1: torch.float8_e4m3fn, 2: torch.bfloat16, 4: torch.float32}.get(dtype.itemsize) or \
+        _fail(f"{what}: pages of {dtype}, which the codec has no type for")
 
 
 def copy_workspace(device="cuda"):
@@ -99,10 +103,11 @@ def copy(src, src_ids, dst, dst_ids, count=None, ws=None, stream=None):
 
 
 class StoredPages:
-    """One sequence's pages as a container of the codec, and its length."""
+    """One sequence's pages as a container of the codec, its length, and what its pages were
+    (planes, shape, type and positions of a page)."""
 
-    def __init__(self, container, length, chunk_bytes):
-        self.container, self.length, self.chunk_bytes = container, length, chunk_bytes
+    def __init__(self, container, length, chunk_bytes, pages):
+        self.container, self.length, self.chunk_bytes, self.pages = container, length, chunk_bytes, pages
 
 
 class PagePool:
@@ -195,6 +200,10 @@ class PagePool:
         n = int(self.lens[row])
         return n, self.tables[row, : -(-n // self.page_tokens)]
 
+    @property
+    def _page(self):
+        return self.pages.shape[0], tuple(self.pages.shape[2:]), self.pages.dtype, self.page_tokens
+
     def store(self, row, chunk_bytes=Z.DEFAULT_CHUNK_BYTES, plan=None):
         """The pages of the sequence in `row`, gathered and compressed (synchronises). The row
         keeps them; free it to give them back."""
@@ -203,19 +212,25 @@ class PagePool:
             _fail("PagePool.store: an empty row")
         flat = self.gather(ids)
         with torch.cuda.device(self.device):
-            c = Z.compress(flat.view(_CODEC.get(flat.dtype, flat.dtype)), chunk_bytes, plan)
-        return StoredPages(c, n, chunk_bytes)
+            c = Z.compress(flat.view(_codec_dtype(flat.dtype, "PagePool.store")), chunk_bytes, plan)
+        return StoredPages(c, n, chunk_bytes, self._page)
 
     def load(self, stored, row):
         """A stored sequence back into the empty `row`, in fresh pages (synchronises)."""
-        before = self.status()
-        Z.check(before, "PagePool.load")
+        if stored.pages != self._page:
+            _fail("PagePool.load: a sequence of pages of another shape, type or length")
+        dt = self.pages.dtype
+        codec = _codec_dtype(dt, "PagePool.load")
+        Z.check(self.status(), "PagePool.load: an earlier call")
         self.fork([row], [-1], [stored.length])
         s = self.status(clear=True)
         Z.check(s, "PagePool.load: no room")
         _, ids = self._held(row)
-        dt = self.pages.dtype
         shape = self.pages.shape[:1] + ids.shape + self.pages.shape[2:]
-        with torch.cuda.device(self.device):
-            flat = Z.decompress(stored.container, _CODEC.get(dt, dt), shape, stored.chunk_bytes)
+        try:
+            with torch.cuda.device(self.device):
+                flat = Z.decompress(stored.container, codec, shape, stored.chunk_bytes)
+        except Z.ZipnnError:  # a damaged container: the row is empty again
+            self.free([row])
+            raise
         self.scatter(flat.view(dt), ids)

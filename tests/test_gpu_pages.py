@@ -330,10 +330,11 @@ def test_offsets_past_32_bits(P):
     assert torch.equal(kv[:, -5:], want)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp8", "fp32", "uint8"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp8", "fp32", "uint8", "int32"])
 def test_store_and_load_through_the_codec(P, Z, dtype):
     """A sequence leaves the cache compressed, its pages go to others, and it comes back."""
-    dt = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp8": torch.float8_e4m3fn, "fp32": torch.float32, "uint8": torch.uint8}[dtype]
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp8": torch.float8_e4m3fn, "fp32": torch.float32, "uint8": torch.uint8,
+          "int32": torch.int32}[dtype]
     g = torch.Generator().manual_seed(2)
     kv = (torch.randn(4, 50, 16, 2, 64, generator=g) * 20).to(dt).cuda()
     pool = P.PagePool(kv, 16, 6, 20)
@@ -358,6 +359,20 @@ def test_store_and_load_through_the_codec(P, Z, dtype):
     with pytest.raises(Z.ZipnnError):
         pool.load(stored, 4)      # no room
     assert pool.status() == Z.OK
+    pool.free([0, 3])
+    other = P.PagePool(kv.view(4, 100, 8, 2, 64), 8, 6, 40)
+    with pytest.raises(Z.ZipnnError):
+        other.load(stored, 0)     # pages of another shape
+    bad = P.StoredPages(stored.container.clone(), stored.length, stored.chunk_bytes, stored.pages)
+    bad.container[:4] = 0
+    books = pool.meta.clone()
+    with pytest.raises(Z.ZipnnError):
+        pool.load(bad, 4)         # a damaged container: the row is empty again
+    assert torch.equal(pool.meta, books) and pool.status() == Z.OK
+    wide = P.PagePool(torch.zeros(1, 2, 4, dtype=torch.int64, device="cuda"), 4, 2, 2)
+    wide.fork([0], [-1], [4])
+    with pytest.raises(Z.ZipnnError):
+        wide.store(0)             # no type of the codec
 
 
 def test_a_cache_in_four_bits_through_the_codec(P):
