@@ -320,8 +320,10 @@ typedef enum { ZIPNN_VALUE_BF16 = 0, ZIPNN_VALUE_FP32 = 1, ZIPNN_VALUE_FP16 = 2 
 size_t zipnn_mx_row_bytes(uint64_t cols);
 /* Bytes of the scale tiles; 0 for invalid arguments. */
 size_t zipnn_mx_scale_bytes(zipnn_mx_format format, uint64_t rows, uint64_t cols);
-/* Workspace bytes of zipnn_mx_quantize with find_global (16-byte aligned, no contents kept). */
+/* Workspace bytes of zipnn_mx_quantize with find_global (16-byte aligned, no contents kept);
+ * none is needed where rows * ceil(cols / 32) is at most ZIPNN_MX_SMALL. */
 #define ZIPNN_MX_WORKSPACE_BYTES 4096u
+#define ZIPNN_MX_SMALL 1024u
 
 /* Quantise the matrix at `x` (device, aligned to its values; row r at x + r * row_stride
  * values, row_stride >= cols) into `codes` and `scales` (device).

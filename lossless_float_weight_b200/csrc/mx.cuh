@@ -2,6 +2,8 @@
 #pragma once
 #include <cstdint>
 
+#include "zipnn.h"
+
 namespace zipnn {
 
 constexpr int kMxFp4 = 0, kNvFp4 = 1;
@@ -23,6 +25,8 @@ constexpr uint64_t kMxMaxRows = 1ull << 31, kMxMaxCols = 1ull << 30, kMxMaxStrid
 inline bool mx_valid(int fmt, uint64_t rows, uint64_t cols) {
   return (fmt == kMxFp4 || fmt == kNvFp4) && rows >= 1 && cols >= 1 && rows <= kMxMaxRows && cols <= kMxMaxCols;
 }
+// Matrices whose largest value every block of a quantisation finds for itself.
+inline bool mx_small(uint64_t rows, uint64_t cols) { return rows <= ZIPNN_MX_SMALL && rows * mx_div_up(cols, 32) <= ZIPNN_MX_SMALL; }
 inline bool mx_valid_type(int t) { return t == kValBF16 || t == kValFP32 || t == kValFP16; }
 __host__ __device__ constexpr uint32_t mx_value_bytes(int t) { return t == kValFP32 ? 4u : 2u; }
 

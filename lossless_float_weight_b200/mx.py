@@ -173,7 +173,9 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
     codes = torch.empty(rows, _row_bytes(cols), dtype=torch.float4_e2m1fn_x2, device=dev)
     scales = torch.empty(_scale_bytes(format, rows, cols), dtype=_SCALE_DTYPES[format], device=dev)
     if rows:
-        ws = torch.empty(Z.MX_WORKSPACE_BYTES, dtype=torch.uint8, device=dev) if find else None
+        ws = None
+        if find and rows * ((cols + 31) // 32) > Z.MX_SMALL:
+            ws = torch.empty(Z.MX_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
         _call(Z.zipnn_mx_quantize, "zipnn_mx_quantize", dev, f, type, m.data_ptr(), rows, cols, stride,
               None if global_scale is None else global_scale.data_ptr(), find, codes.data_ptr(), scales.data_ptr(),
               None if ws is None else ws.data_ptr(), Z.MX_WORKSPACE_BYTES)

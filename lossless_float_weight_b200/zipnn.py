@@ -85,6 +85,7 @@ zipnn_shard_tables = _sig("zipnn_shard_tables", _i, _i, _u32, _u32, ctypes.POINT
 MXFP4, NVFP4 = 0, 1
 VALUE_BF16, VALUE_FP32, VALUE_FP16 = 0, 1, 2
 MX_WORKSPACE_BYTES = 4096
+MX_SMALL = 1024
 
 zipnn_mx_row_bytes = _sig("zipnn_mx_row_bytes", _sz, _u64)
 zipnn_mx_scale_bytes = _sig("zipnn_mx_scale_bytes", _sz, _i, _u64, _u64)

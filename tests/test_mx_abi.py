@@ -27,7 +27,7 @@ def test_sizes(Z):
 def test_argument_errors_without_a_device(Z):
     fake, ws = 1 << 20, Z.MX_WORKSPACE_BYTES  # never dereferenced: every case fails before a launch
 
-    def quant(fmt=Z.NVFP4, t=Z.VALUE_BF16, x=fake, rows=4, cols=64, stride=64, g=fake, find=1, codes=fake, scales=fake,
+    def quant(fmt=Z.NVFP4, t=Z.VALUE_BF16, x=fake, rows=513, cols=64, stride=64, g=fake, find=1, codes=fake, scales=fake,
               w=fake, wb=ws):
         return Z.zipnn_mx_quantize(fmt, t, x, rows, cols, stride, g, find, codes, scales, w, wb, None)
 
@@ -57,6 +57,8 @@ def test_argument_errors_without_a_device(Z):
         assert Z.zipnn_mx_status(None) == Z.ERR_UNSUPPORTED
         assert quant() == Z.ERR_UNSUPPORTED and deq() == Z.ERR_UNSUPPORTED
         assert quant(fmt=Z.MXFP4, g=None, w=None, wb=0) == Z.ERR_UNSUPPORTED  # not needed for MXFP4
+        assert quant(rows=512, w=None, wb=0) == Z.ERR_UNSUPPORTED  # nor for 1024 chunks
+        assert quant(find=0, w=None, wb=0) == Z.ERR_UNSUPPORTED
 
 
 def test_python_refusals(Z):
