@@ -352,7 +352,7 @@ zipnn_status zipnn_mx_dequantize(zipnn_mx_format format, zipnn_value_type type, 
 /* out = A B^T for microscaled matrices of one format, A of m rows and B of n rows of k values:
  * out (device, aligned to its values; row i at out + i * row_stride values) receives m rows of
  * n. Products and scales are exact, sums are FP32 (the tensor cores' own), for NVFP4 times
- * *a_global and *b_global, then rounded once to `type`. The order of a sum depends on the
+ * the product of *a_global and *b_global, then rounded once to `type`. The order of a sum depends on the
  * sizes alone, so equal calls give equal bits. A NaN scale makes its row's results NaN.
  * At most 2^31 - 1 tiles of 128 x 128. Asynchronous, no workspace; a device-side wait that
  * gives up (never expected) leaves its part of `out` unwritten and sets the device's status. */

@@ -189,13 +189,36 @@ __device__ __forceinline__ void put(T* out, uint64_t step, uint32_t n, const flo
       if ((uint32_t)c < n) out[c * step] = to_value<T>(v[c]);
   }
 }
+// The product of the two tensors' scales (NVFP4): in FP32 where it is an ordinary number, else
+// the sums are scaled in 64 bits, so that neither scale alone takes a result out of range.
+struct Scale {
+  float f;
+  double d;
+  bool usual;
+};
+template <int FMT>
+__device__ __forceinline__ Scale scale_of(const Args& a) {
+  Scale s = {1.f, 1.0, true};
+  if constexpr (FMT == kNvFp4) {
+    s.d = (double)*a.ga * (double)*a.gb;
+    s.f = (float)s.d;
+    s.usual = s.d >= 1e-36 && s.d <= 1e36;
+  }
+  return s;
+}
+
 // The sums of row p of P and rows q .. q + N - 1 of Q, scaled and rounded.
 template <int FMT, int N>
-__device__ __forceinline__ void store(const Args& a, uint32_t p, uint32_t q, float* v, float g0, float g1) {
+__device__ __forceinline__ void store(const Args& a, uint32_t p, uint32_t q, float* v, const Scale& g) {
   if (p >= a.p_rows || q >= a.q_rows) return;
   if constexpr (FMT == kNvFp4) {
+    if (g.usual) {
 #pragma unroll
-    for (int c = 0; c < N; c++) v[c] = v[c] * g0 * g1;
+      for (int c = 0; c < N; c++) v[c] *= g.f;
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; c++) v[c] = (float)((double)v[c] * g.d);
+    }
   }
   const uint64_t at = a.p_is_n ? (uint64_t)q * a.ldo + p : (uint64_t)p * a.ldo + q, step = a.p_is_n ? a.ldo : 1;
   if (a.type == kValFP32) put<float, N>(reinterpret_cast<float*>(a.out) + at, step, a.q_rows - q, v);
@@ -209,7 +232,7 @@ __device__ __forceinline__ void store(const Args& a, uint32_t p, uint32_t q, flo
 // microsecond).
 template <int FMT, int SPLIT>
 __device__ __forceinline__ void add_peers(const Args& a, const float4* sums, uint32_t rank, uint32_t used, uint32_t p, uint32_t q,
-                                          float g0, float g1) {
+                                          const Scale& g) {
   constexpr uint32_t kAtOnce = 8 / SPLIT;
   for (uint32_t c = rank * 4; c < used; c += kAtOnce * SPLIT * 4) {
     float4 t[kAtOnce][SPLIT];
@@ -224,7 +247,7 @@ __device__ __forceinline__ void add_peers(const Args& a, const float4* sums, uin
       float4 v = t[k][0];
 #pragma unroll
       for (int r = 1; r < SPLIT; r++) v.x += t[k][r].x, v.y += t[k][r].y, v.z += t[k][r].z, v.w += t[k][r].w;
-      store<FMT, 4>(a, p, q + c + k * SPLIT * 4, &v.x, g0, g1);
+      store<FMT, 4>(a, p, q + c + k * SPLIT * 4, &v.x, g);
     }
   }
 }
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
     if (threadIdx.x == 0) atomicMax(&g_mx_status, kStTimeout);
   }
   const bool ok = *failed == 0;
-  const float g0 = FMT == kNvFp4 ? *a.ga : 1.f, g1 = FMT == kNvFp4 ? *a.gb : 1.f;
+  const Scale g = scale_of<FMT>(a);
   const uint32_t used = min((uint32_t)BN, a.q_rows - q0);  // columns that the output has
   if (a.split == 1) {
     if (warp < 4 && ok) {
@@ -342,7 +365,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
       for (uint32_t c = 0; c < used; c += 16) {
         float v[16];
         load_sums(tmem + (warp * 32 << 16) + c, v);
-        store<FMT, 16>(a, p0 + threadIdx.x, q0 + c, v, g0, g1);
+        store<FMT, 16>(a, p0 + threadIdx.x, q0 + c, v, g);
       }
     }
   } else {
@@ -361,9 +384,9 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
     cluster_sync();
     if (warp < 4 && ok) {
       const uint32_t p = p0 + threadIdx.x;
-      if (a.split == 2) add_peers<FMT, 2>(a, sums, rank, used, p, q0, g0, g1);
-      else if (a.split == 4) add_peers<FMT, 4>(a, sums, rank, used, p, q0, g0, g1);
-      else add_peers<FMT, 8>(a, sums, rank, used, p, q0, g0, g1);
+      if (a.split == 2) add_peers<FMT, 2>(a, sums, rank, used, p, q0, g);
+      else if (a.split == 4) add_peers<FMT, 4>(a, sums, rank, used, p, q0, g);
+      else add_peers<FMT, 8>(a, sums, rank, used, p, q0, g);
     }
     cluster_sync();
   }
@@ -568,7 +591,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
       __syncwarp();
     }
   } else if (warp < 8) {
-    const float g = FMT == kNvFp4 ? *a.ga : 1.f, g1 = FMT == kNvFp4 ? *a.gb : 1.f;
+    const Scale g = scale_of<FMT>(a);
     const uint32_t quarter = warp % 4, half = warp / 4, leader_bar = peer(smem_addr(sums_empty), 0);
     constexpr int kCols = BN / 2;  // of one warp
     uint32_t k_tile = 0;
@@ -586,7 +609,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive_at(leader_bar);
-      if (!*failed) store<FMT, kCols>(a, p, q, v, g, g1);
+      if (!*failed) store<FMT, kCols>(a, p, q, v, g);
     }
     __syncwarp();
   }

@@ -127,6 +127,19 @@ def test_an_output_past_32_bits(mx, m, n):
     assert np.array_equal(got, torch.from_numpy(want).to(torch.bfloat16).double().numpy())
 
 
+@pytest.mark.parametrize("m,n", [(3, 200), (100, 300), (1700, 1600)])
+@pytest.mark.parametrize("ga,gb", [(-100, 100), (-140, 120), (-30, -90), (-126, -10), (60, 60)])
+def test_scales_of_far_apart_tensors(mx, m, n, ga, gb):
+    """Powers of two, so that the sums stay exact: no scale alone takes a result out of range."""
+    a, va = random_mx(mx, m, 96, "nvfp4", 1, exact=True)
+    b, vb = random_mx(mx, n, 96, "nvfp4", 2, exact=True)
+    a.global_scale.fill_(2.0 ** ga)
+    b.global_scale.fill_(2.0 ** gb)
+    y = mx.matmul(a, b, torch.float32).double().cpu().numpy()
+    with np.errstate(over="ignore"):
+        assert np.array_equal(y, (va @ vb.T * 2.0 ** (ga + gb)).astype(np.float32).astype(np.float64))
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_nan_blocks_stay_in_their_rows(mx, fmt):
     g = torch.Generator().manual_seed(1)
