@@ -41,18 +41,18 @@ def _pool_desc(t, what):
     if not t.is_cuda or t.dim() < 3:
         _fail(f"{what}: a CUDA tensor (planes, pages, ...)")
     shape, size = t.shape, t.element_size()
-    n = 1
+    planes, count = shape[0], shape[1]
     if t.is_contiguous():
-        n = t.numel() // max(1, shape[0] * shape[1])
-    else:
-        for d in range(t.dim() - 1, 1, -1):
-            if shape[d] != 1 and t.stride(d) != n:
-                _fail(f"{what}: pages are contiguous")
-            n *= shape[d]
+        page = t.numel() * size // (planes * count or 1)
+        return Z.PagePoolDesc(t.data_ptr(), page * count, page, planes, count), page
+    n = 1
+    for d in range(t.dim() - 1, 1, -1):
+        if shape[d] != 1 and t.stride(d) != n:
+            _fail(f"{what}: pages are contiguous")
+        n *= shape[d]
     # the stride of a dimension of one element says nothing
-    page = t.stride(1) * size if shape[1] > 1 else n * size
-    plane = t.stride(0) * size if shape[0] > 1 else page * shape[1]
-    return Z.PagePoolDesc(t.data_ptr(), plane, page, shape[0], shape[1]), n * size
+    page = t.stride(1) * size if count > 1 else n * size
+    return Z.PagePoolDesc(t.data_ptr(), t.stride(0) * size if planes > 1 else page * count, page, planes, count), n * size
 
 
 def _ids(v, device, what):
@@ -76,14 +76,15 @@ def copy(src, src_ids, dst, dst_ids, count=None, ws=None, stream=None):
     b, nb = _pool_desc(dst, "pages.copy: dst")
     if na != nb or src.device != dst.device or a.planes != b.planes:
         _fail("pages.copy: src and dst have the same planes and page size, on one device")
+    n = min(a.pages, b.pages)
     if src_ids is not None:
         src_ids = _ids(src_ids, dst.device, "pages.copy: src_ids")
+        n = src_ids.numel()
     if dst_ids is not None:
         dst_ids = _ids(dst_ids, dst.device, "pages.copy: dst_ids")
-    lists = [v.numel() for v in (src_ids, dst_ids) if v is not None]
-    n = min(lists) if lists else min(a.pages, b.pages)
-    if n != max(lists, default=n):
-        _fail("pages.copy: as many destinations as sources")
+        if src_ids is not None and dst_ids.numel() != n:
+            _fail("pages.copy: as many destinations as sources")
+        n = dst_ids.numel()
     if count is not None:
         if not 0 <= count <= n:
             _fail("pages.copy: count is at most the lists' length")
