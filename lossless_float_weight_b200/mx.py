@@ -147,18 +147,22 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
     if stream is not None:
         with _use(stream, x.device):
             return quantize(x, format, global_scale)
-    f, type = _format(format), _VALUES.get(x.dtype)
-    if type is None or not x.is_cuda or x.dim() == 0 or x.shape[-1] == 0:
+    f, type, shape = _format(format), _VALUES.get(x.dtype), tuple(x.shape)
+    if type is None or not x.is_cuda or not shape or shape[-1] == 0:
         _fail("mx.quantize: a CUDA tensor (..., K) of BF16, FP16 or FP32")
     if x.requires_grad and torch.is_grad_enabled():
         _fail("mx.quantize: no gradient passes through it; detach x or use torch.no_grad()")
-    shape, dev = tuple(x.shape), x.device
-    cols = shape[-1]
-    m = x if len(shape) == 2 else x.reshape(-1, cols)
-    rows = m.shape[0]
-    stride = m.stride(0) if rows > 1 else cols
-    if (cols > 1 and m.stride(1) != 1) or stride < cols:
-        m, stride = m.contiguous(), cols
+    dev, cols = x.device, shape[-1]
+    if len(shape) == 2:
+        m, rows = x, shape[0]
+    else:
+        m = x.reshape(-1, cols)
+        rows = m.shape[0]
+    stride = cols
+    if not m.is_contiguous():
+        stride = m.stride(0) if rows > 1 else cols
+        if (cols > 1 and m.stride(1) != 1) or stride < cols:
+            m, stride = m.contiguous(), cols
     find = False
     if f == Z.NVFP4:
         find = global_scale is None
