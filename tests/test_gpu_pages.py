@@ -276,6 +276,22 @@ def test_books_of_every_size(P, pages):
     assert b.fork([0], [-1], [per])
 
 
+def test_the_longest_lists(P):
+    """2^18 rows, forked, freed and closed up in one call each, and 200,000 pairs copied."""
+    seqs = 1 << 18
+    b = Both(P, 1, 300_000, 1, (1, 4), seqs, 2)
+    rng = np.random.RandomState(1)
+    assert b.fork(rng.permutation(seqs).tolist(), [-1] * seqs, [1] * seqs)
+    assert not b.fork([0, seqs], [0, -1], [2, 1])
+    b.free(rng.permutation(seqs)[: seqs // 2].tolist(), compact=True)
+    filled = np.nonzero(b.books.lens)[0]
+    assert b.fork(filled[:1000].tolist(), filled[:1000].tolist(), [2] * 1000)
+    perm = torch.from_numpy(rng.permutation(300_000).astype(np.int32)).cuda()
+    src = b.pool.pages.clone()
+    out = P.copy(src, perm[:200_000], torch.zeros_like(src), perm[100_000:])
+    assert torch.equal(out[:, perm[100_000:].long()], src[:, perm[:200_000].long()])
+
+
 def test_two_pools_two_streams_and_graphs(P, Z):
     pools = [Both(P, 2, 64, 4, (4, 8), 8, 10, s) for s in range(2)]
     for b in pools:
