@@ -236,6 +236,39 @@ def test_through_the_codec(mx, fmt):
     assert torch.equal(mx.dequantize(r), mx.dequantize(q))
 
 
+def test_through_the_codec_with_a_plan(mx):
+    """An FP4 plan made on one weight's codes codes another's."""
+    from lossless_float_weight_b200 import zipnn as Z
+    a, b = (mx.quantize(make(256, 1024, "bf16", s).cuda()) for s in (20, 21))
+    plan = Z.Plan.create(a.codes, groups=2, chunk_bytes=16384)
+    c = mx.compress(b, chunk_bytes=16384, plan=plan)
+    r = mx.decompress(c)
+    assert torch.equal(r.codes.view(torch.uint8), b.codes.view(torch.uint8))
+    assert torch.equal(mx.dequantize(r), mx.dequantize(b))
+
+
+def test_kernel_timing_counts_the_launches(mx):
+    from lossless_float_weight_b200 import pages, zipnn as Z
+    x = make(300, 512, "bf16", 1).cuda()
+    kv = torch.zeros(2, 8, 16, 8, device="cuda")
+    pool = pages.PagePool(kv, 16, 4, 4)
+    torch.cuda.synchronize()
+    Z.kernel_times()
+    assert Z.zipnn_timing_enable(1) == Z.OK
+    try:
+        q = mx.quantize(x, "nvfp4")
+        mx.dequantize(q)
+        mx.matmul(q, q)
+        pool.fork([0], [-1], [20])
+        pool.free([0], compact=True)
+        t = Z.kernel_times()
+    finally:
+        Z.zipnn_timing_enable(0)
+    got = {k: n for k, (ms, n) in t.items() if n}
+    assert got == {"mx_amax": 1, "mx_quantize": 1, "mx_dequantize": 1, "mx_matmul": 1, "pages_plan": 3, "pages_move": 2}
+    assert all(ms > 0 for ms, n in t.values() if n)
+
+
 def test_block_scales_and_from_parts(mx):
     x = make(150, 333, "fp32", 5).cuda()
     for fmt in ("mxfp4", "nvfp4"):

@@ -329,6 +329,30 @@ def test_two_pools_two_streams_and_graphs(P, Z):
     b.same()
 
 
+def test_copies_captured_and_replayed(P, Z):
+    """A checked copy in a graph: the lists are read at each replay, and a bad one copies nothing
+    and is seen in the status."""
+    src, dst = values(3, 20, (8, 4)).cuda(), torch.zeros(3, 20, 8, 4, dtype=torch.int32, device="cuda")
+    a, b = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([1, 2, 3], [4, 5, 6]))
+    ws = P.copy_workspace()
+    P.copy(src, a, dst, b, ws=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        P.copy(src, a, dst, b, ws=ws)
+        P.copy(dst, b, dst, a, ws=ws)
+    for x, y in (([1, 2, 3], [4, 5, 6]), ([7, 7, 19], [0, 9, 18]), ([0, 1, 2], [3, 3, 4]), ([5, 6, 8], [11, 12, 13])):
+        a.copy_(torch.tensor(x, dtype=torch.int32))
+        b.copy_(torch.tensor(y, dtype=torch.int32))
+        want = dst.clone()
+        if len(set(y)) == 3:  # a page named twice is refused as a destination, not as a source
+            want[:, y] = src[:, x]
+        if len(set(x)) == 3:
+            want[:, x] = want[:, y].clone()
+        g.replay()
+        assert torch.equal(dst, want)
+    assert Z.status(ws) == Z.ERR_INVALID_ARG
+
+
 def test_offsets_past_32_bits(P):
     """A pool of 9.7 GB: its last pages, gathered, moved and scattered."""
     kv = torch.empty(3, 100_000, 16, 1024, dtype=torch.bfloat16, device="cuda")
