@@ -566,8 +566,9 @@ __global__ void __launch_bounds__(kThreads) k_mx_dequantize_any(Packed m, uint8_
     const uint32_t bits[2] = {__funnelshift_r(c0, c1, sh), __funnelshift_r(c1, c2, sh)};
     const int b0 = lo / kBlk, b1 = (hi - 1) / kBlk;
     const uint8_t* st = m.scales + row / 128 * m.col_tiles * kMxTileBytes + mx_in_tile(row % 128, 0);
-    const float s0 = scale_of<FMT>(__ldg(st + (uint32_t)(b0 / 4) * kMxTileBytes + b0 % 4));
-    const float s1 = b1 == b0 ? s0 : scale_of<FMT>(__ldg(st + (uint32_t)(b1 / 4) * kMxTileBytes + b1 % 4));
+    // a row's tiles pass 32 bits: 2^30 columns of NVFP4 have 8 GB of them
+    const float s0 = scale_of<FMT>(__ldg(st + (uint64_t)(b0 / 4) * kMxTileBytes + b0 % 4));
+    const float s1 = b1 == b0 ? s0 : scale_of<FMT>(__ldg(st + (uint64_t)(b1 / 4) * kMxTileBytes + b1 % 4));
     const int cut = (b0 + 1) * kBlk - e0;  // values from here on are of the second block
     float v[kReadBack];
 #pragma unroll

@@ -1,0 +1,53 @@
+"""Microscaled 4-bit tensors at the ends of what a call takes: the longest rows, inputs that
+carry gradients or a pending sign, and what a stored tensor shares with the one it came from."""
+import numpy as np
+import pytest
+import torch
+
+import mx_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mx():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from lossless_float_weight_b200 import mx
+    return mx
+
+
+@pytest.fixture(scope="module")
+def Z():
+    from lossless_float_weight_b200 import zipnn
+    return zipnn
+
+
+@pytest.mark.parametrize("fmt,cols", [("nvfp4", (1 << 29) + 65), ("nvfp4", 1 << 30), ("nvfp4", (1 << 30) - 7), ("mxfp4", (1 << 30) - 7)])
+def test_the_longest_rows(mx, fmt, cols):
+    """One row whose scale tiles pass 2^32 bytes (NVFP4, from column 2^29 on): both its ends,
+    the middle, and the zeros between them. A power of two as the global scale, so that values
+    read back as they are."""
+    g = 0.25 if fmt == "nvfp4" else None
+    gt = None if g is None else torch.tensor([g], device="cuda")
+    x = torch.zeros(1, cols, dtype=torch.bfloat16, device="cuda")
+    rng = torch.Generator().manual_seed(cols % 1000)
+    spans = [(0, 192), ((cols // 2) // 128 * 128, 192), (cols // 64 * 64 - 256, cols - (cols // 64 * 64 - 256))]
+    parts = []
+    for k, (at, n) in enumerate(spans):  # of different sizes, so that one end's scales are not the other's
+        p = (torch.randn(1, n, generator=rng) * 5.0 ** k).to(torch.bfloat16)
+        x[:, at:at + n] = p.cuda()
+        parts.append(U.quantize(p.double().numpy(), fmt, g))
+    q = mx.quantize(x, fmt, gt)
+    y = mx.dequantize(q, torch.bfloat16, out=x)  # in place of the values: the memory is large
+    for (at, n), (code, byte, _) in zip(spans, parts):
+        got, _ = U.unpack(q.codes.view(torch.uint8)[:, at // 2:(at + n + 1) // 2].cpu().numpy(), 1, n)
+        assert np.array_equal(got, code)
+        blk = U.BLOCK[fmt]
+        b = np.arange(at // blk, at // blk + byte.shape[1])
+        sc = q.scales.view(torch.uint8)[torch.from_numpy(512 * (b // 4) + b % 4).cuda()].cpu().numpy()
+        assert np.array_equal(sc, byte[0])
+        want = torch.from_numpy(U.values(code, byte, fmt, g)).to(torch.bfloat16)
+        assert torch.equal(y[:, at:at + n].cpu(), want)
+    for (at, n), (then, _) in zip(spans, spans[1:]):
+        assert not y[:, at + n:then].any()
