@@ -207,10 +207,16 @@ class PagePool:
 
     def store(self, row, chunk_bytes=Z.DEFAULT_CHUNK_BYTES, plan=None):
         """The pages of the sequence in `row`, gathered and compressed (synchronises). The row
-        keeps them; free it to give them back."""
+        keeps them; free it to give them back. A row whose length or page numbers do not fit the
+        pool is refused with Z.ERR_CORRUPT."""
         n, ids = self._held(row)
         if n == 0:
             _fail("PagePool.store: an empty row")
+        # a row that the pool's own calls would report as damaged: what gather leaves of such
+        # pages is whatever was in the memory
+        held = -(-n // self.page_tokens)
+        if n < 0 or held > self._table.slots or not all(0 <= p < self._pool.pages for p in ids.tolist()):
+            raise Z.ZipnnError(Z.ERR_CORRUPT, f"PagePool.store: row {row}")
         flat = self.gather(ids)
         with torch.cuda.device(self.device):
             c = Z.compress(flat.view(_codec_dtype(flat.dtype, "PagePool.store")), chunk_bytes, plan)

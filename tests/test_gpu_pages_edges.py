@@ -1,0 +1,62 @@
+"""Pages of a K/V cache: stores of rows that are damaged."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def P():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from lossless_float_weight_b200 import pages
+    return pages
+
+
+@pytest.fixture(scope="module")
+def Z():
+    from lossless_float_weight_b200 import zipnn
+    return zipnn
+
+
+def cache(P, planes=2, pages=20, seed=0):
+    kv = torch.randn(planes, pages, 16, 2, 64, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+    return P.PagePool(kv, 16, 6, 8)
+
+
+@pytest.mark.parametrize("number", [99, 20, -7, -1])
+def test_a_damaged_row_is_not_stored(P, Z, number):
+    """A number outside the pool in the row's table, in the row itself and in a fork of it."""
+    pool = cache(P)
+    pool.fork([0, 1], [-1, -1], [70, 33])
+    whole = pool.store(1)
+    pool.tables[0, 2] = number
+    pool.fork([2], [0], [64])
+    assert pool.status(clear=True) == Z.ERR_CORRUPT
+    for row in (0, 2):
+        with pytest.raises(Z.ZipnnError) as e:
+            pool.store(row)
+        assert e.value.status == Z.ERR_CORRUPT
+    assert pool.status() == Z.OK and torch.equal(pool.store(1).container, whole.container)
+
+
+@pytest.mark.parametrize("length", [129, 1 << 30, -5])
+def test_a_row_of_an_impossible_length_is_not_stored(P, Z, length):
+    pool = cache(P)
+    pool.fork([0], [-1], [128])
+    pool.lens[0] = length
+    with pytest.raises(Z.ZipnnError) as e:
+        pool.store(0)
+    assert e.value.status == Z.ERR_CORRUPT
+
+
+def test_a_store_beside_an_earlier_error(P, Z):
+    """An error that was not yet taken stays for its caller, and says nothing of the store."""
+    pool = cache(P)
+    pool.fork([0], [-1], [70])
+    pool.fork([0], [-1], [70])  # refused: the row is filled
+    stored = pool.store(0)
+    assert pool.status(clear=True) == Z.ERR_INVALID_ARG
+    want = pool.gather(pool.tables[0, :5]).clone()
+    pool.load(stored, 3)
+    assert torch.equal(pool.gather(pool.tables[3, :5]), want)
