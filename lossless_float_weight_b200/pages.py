@@ -226,18 +226,20 @@ class PagePool:
         """A stored sequence back into the empty `row`, in fresh pages (synchronises)."""
         if stored.pages != self._page:
             _fail("PagePool.load: a sequence of pages of another shape, type or length")
+        if stored.container.device != self.device:
+            _fail(f"PagePool.load: a sequence on {stored.container.device}, pages on {self.device}")
         dt = self.pages.dtype
         codec = _codec_dtype(dt, "PagePool.load")
         Z.check(self.status(), "PagePool.load: an earlier call")
+        # decoded before the row takes its pages: what can fail there (a damaged container, no
+        # memory) then changes nothing
+        shape = self.pages.shape[:1] + (-(-stored.length // self.page_tokens),) + self.pages.shape[2:]
+        with torch.cuda.device(self.device):
+            flat = Z.decompress(stored.container, codec, shape, stored.chunk_bytes).view(dt)
         self.fork([row], [-1], [stored.length])
-        s = self.status(clear=True)
-        Z.check(s, "PagePool.load: no room")
-        _, ids = self._held(row)
-        shape = self.pages.shape[:1] + ids.shape + self.pages.shape[2:]
+        Z.check(self.status(clear=True), "PagePool.load: no room")
         try:
-            with torch.cuda.device(self.device):
-                flat = Z.decompress(stored.container, codec, shape, stored.chunk_bytes)
-        except Z.ZipnnError:  # a damaged container: the row is empty again
+            copy(flat, None, self.pages, self._held(row)[1])  # with a status of its own: waits, and raises
+        except BaseException:  # whatever it was, the row is empty again
             self.free([row])
             raise
-        self.scatter(flat.view(dt), ids)

@@ -1,4 +1,4 @@
-"""Pages of a K/V cache: stores of rows that are damaged."""
+"""Pages of a K/V cache: stores of rows that are damaged, loads that fail."""
 import pytest
 import torch
 
@@ -60,3 +60,38 @@ def test_a_store_beside_an_earlier_error(P, Z):
     want = pool.gather(pool.tables[0, :5]).clone()
     pool.load(stored, 3)
     assert torch.equal(pool.gather(pool.tables[3, :5]), want)
+
+
+@pytest.mark.parametrize("where", ["decompress", "scatter"])
+@pytest.mark.parametrize("error", [torch.cuda.OutOfMemoryError, KeyboardInterrupt, RuntimeError])
+def test_a_load_that_fails_leaves_the_books_as_they_were(P, Z, monkeypatch, where, error):
+    pool = cache(P)
+    pool.fork([0, 1], [-1, -1], [70, 33])
+    stored = pool.store(0)
+    pool.free([0])
+    books = pool.meta.clone()
+
+    def fail(*a, **k):
+        raise error("out of memory")
+
+    with monkeypatch.context() as m:
+        if where == "decompress":
+            m.setattr(Z, "decompress", fail)
+        else:
+            m.setattr(P, "copy", fail)
+        with pytest.raises(error):
+            pool.load(stored, 2)
+    assert torch.equal(pool.meta, books) and pool.status() == Z.OK
+    pool.load(stored, 2)
+    assert pool.lens.tolist() == [0, 33, 70, 0, 0, 0]
+
+
+def test_a_stored_sequence_on_another_device_is_refused(P, Z):
+    pool = cache(P)
+    pool.fork([0], [-1], [70])
+    stored = pool.store(0)
+    books = pool.meta.clone()
+    away = P.StoredPages(stored.container.cpu(), stored.length, stored.chunk_bytes, stored.pages)
+    with pytest.raises(Z.ZipnnError):
+        pool.load(away, 2)
+    assert torch.equal(pool.meta, books)
