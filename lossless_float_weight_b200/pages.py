@@ -16,6 +16,7 @@ sequence holds which page (the references, lengths and tables of include/zipnn.h
 `stream`); what they find wrong is read with `status()`. `store` and `load` synchronise.
 """
 import ctypes
+import math
 
 import torch
 
@@ -43,7 +44,8 @@ def _pool_desc(t, what):
     shape, size = t.shape, t.element_size()
     planes, count = shape[0], shape[1]
     if t.is_contiguous():
-        page = t.numel() * size // (planes * count or 1)
+        n = planes * count
+        page = t.numel() * size // n if n else math.prod(shape[2:]) * size
         return Z.PagePoolDesc(t.data_ptr(), page * count, page, planes, count), page
     n = 1
     for d in range(t.dim() - 1, 1, -1):

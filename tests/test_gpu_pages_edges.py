@@ -1,4 +1,4 @@
-"""Pages of a K/V cache: stores of rows that are damaged, loads that fail."""
+"""Pages of a K/V cache: stores of rows that are damaged, loads that fail, lists of no pages."""
 import pytest
 import torch
 
@@ -95,3 +95,20 @@ def test_a_stored_sequence_on_another_device_is_refused(P, Z):
     with pytest.raises(Z.ZipnnError):
         pool.load(away, 2)
     assert torch.equal(pool.meta, books)
+
+
+def test_lists_of_no_pages(P, Z):
+    pool = cache(P)
+    pool.fork([0], [-1], [0])
+    none = pool.gather(pool.tables[0, :0])
+    assert none.shape == (2, 0, 16, 2, 64) and none.dtype == torch.bfloat16
+    assert pool.gather([]).shape == none.shape
+    before = pool.pages.clone()
+    pool.scatter(none, [])
+    pool.scatter(none, torch.empty(0, dtype=torch.int32, device="cuda"))
+    P.copy(none, None, pool.pages, None)
+    P.copy(pool.pages, [], none, [])
+    assert torch.equal(pool.pages, before) and pool.status() == Z.OK
+    for bad in (lambda: P.copy(none[..., :32], None, pool.pages, None), lambda: pool.scatter(none[:1], [])):
+        with pytest.raises(Z.ZipnnError):
+            bad()
