@@ -141,8 +141,9 @@ def tile_scales(block_scales):
 def quantize(x, format="mxfp4", global_scale=None, stream=None):
     """Quantise the CUDA tensor x (..., K) in blocks along its last dimension.
 
-    nvfp4: global_scale is a one-element FP32 CUDA tensor (positive; taken as it is), or None:
-    then it is found from x (its largest finite magnitude / 2688). Rounding, saturation and
+    nvfp4: global_scale is a one-element FP32 CUDA tensor (positive; taken as it is, and kept by
+    the result, whose values change with it), or None: then it is found from x (its largest
+    finite magnitude / 2688). Rounding, saturation and
     what a block with a NaN gives: zipnn_mx_quantize."""
     if stream is not None:
         with _use(stream, x.device):
@@ -272,7 +273,9 @@ def compress(q, chunk_bytes=Z.DEFAULT_CHUNK_BYTES, plan=None, stream=None):
     with torch.cuda.device(q.device):
         codes = Z.compress(q.codes.view(torch.float4_e2m1fn_x2), chunk_bytes, plan, stream=stream)
         scales = Z.compress(q.scales.view(torch.float8_e4m3fn), chunk_bytes, stream=stream)
-    return MxContainers(codes, scales, q.shape, q.format, q.global_scale, chunk_bytes)
+        # a copy, as of the codes: what becomes of q does not reach what is stored
+        g = None if q.global_scale is None else q.global_scale.clone()
+    return MxContainers(codes, scales, q.shape, q.format, g, chunk_bytes)
 
 
 def decompress(c, stream=None):
@@ -282,4 +285,5 @@ def decompress(c, stream=None):
         codes = Z.decompress(c.codes, torch.float4_e2m1fn_x2, (rows, Z.zipnn_mx_row_bytes(cols)), c.chunk_bytes, stream)
         scales = Z.decompress(c.scales, torch.float8_e4m3fn, (Z.zipnn_mx_scale_bytes(_FORMATS[c.format], rows, cols),),
                               c.chunk_bytes, stream)
-    return MxTensor(codes, scales.view(_SCALE_DTYPES[c.format]), c.shape, c.format, c.global_scale)
+        g = None if c.global_scale is None else c.global_scale.clone()
+    return MxTensor(codes, scales.view(_SCALE_DTYPES[c.format]), c.shape, c.format, g)

@@ -51,3 +51,17 @@ def test_the_longest_rows(mx, fmt, cols):
         assert torch.equal(y[:, at:at + n].cpu(), want)
     for (at, n), (then, _) in zip(spans, spans[1:]):
         assert not y[:, at + n:then].any()
+
+
+def test_a_stored_tensor_keeps_its_own_scale(mx):
+    """What happens to the scale of the tensor that was stored, or of one that was loaded, does
+    not reach the container."""
+    x = torch.randn(64, 96, generator=torch.Generator().manual_seed(3)).cuda()
+    q = mx.quantize(x, "nvfp4")
+    want = mx.dequantize(q, torch.float32)
+    c = mx.compress(q)
+    q.global_scale.mul_(3)
+    a = mx.decompress(c)
+    assert torch.equal(mx.dequantize(a, torch.float32), want)
+    a.global_scale.mul_(5)
+    assert torch.equal(mx.dequantize(mx.decompress(c), torch.float32), want)
