@@ -153,6 +153,8 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
         _fail("mx.quantize: a CUDA tensor (..., K) of BF16, FP16 or FP32")
     if x.requires_grad and torch.is_grad_enabled():
         _fail("mx.quantize: no gradient passes through it; detach x or use torch.no_grad()")
+    if type != Z.VALUE_BF16 and x.is_neg():
+        x = x.resolve_neg()  # a part of a conjugated complex tensor (of which BF16 has none)
     dev, cols = x.device, shape[-1]
     if len(shape) == 2:
         m, rows = x, shape[0]
@@ -193,6 +195,8 @@ def _out(out, shape, dtype, device, what):
     """The caller's tensor where it can be written: its last dimension contiguous."""
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
         _fail(f"{what}: out is a {dtype} tensor {tuple(shape)} on {device}")
+    if out.is_neg():
+        _fail(f"{what}: out is a negated view")
     if not (out.is_contiguous() or (out.dim() == 2 and (out.shape[1] == 1 or out.stride(1) == 1) and out.stride(0) >= out.shape[1])):
         _fail(f"{what}: out's rows are contiguous and do not overlap")
     return out

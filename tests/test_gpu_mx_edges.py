@@ -65,3 +65,17 @@ def test_a_stored_tensor_keeps_its_own_scale(mx):
     assert torch.equal(mx.dequantize(a, torch.float32), want)
     a.global_scale.mul_(5)
     assert torch.equal(mx.dequantize(mx.decompress(c), torch.float32), want)
+
+
+def test_a_pending_negation_is_taken(mx, Z):
+    """The imaginary part of a conjugate is a view whose sign is not in its memory."""
+    z = torch.view_as_complex(torch.randn(40, 1, 2, generator=torch.Generator().manual_seed(1)).cuda())
+    x = z.conj().imag
+    assert x.is_neg()
+    for view in (x, x[:1], x.t()):
+        for fmt in ("mxfp4", "nvfp4"):
+            a, b = mx.quantize(view, fmt), mx.quantize(view.clone(), fmt)
+            assert torch.equal(a.codes.view(torch.uint8), b.codes.view(torch.uint8))
+    q = mx.quantize(x)
+    with pytest.raises(Z.ZipnnError):
+        mx.dequantize(q, torch.float32, out=z.conj().imag)
