@@ -14,9 +14,11 @@ quantised weight or K/V cache goes through :func:`compress` and comes back bit f
 The functions check their arguments, allocate with PyTorch and call the CUDA library on
 the current stream of the tensors' device (or `stream`); they do not synchronise, except
 :func:`compress` and :func:`decompress`, as the codec's own. They are for stored and served
-tensors: no gradient passes through them, and an input that asks for one is refused.
+tensors: no gradient passes through them, and an input or output that asks for one, in
+reverse or forward mode, is refused.
 """
 import torch
+from torch.autograd import forward_ad
 
 from . import zipnn as Z
 
@@ -33,6 +35,14 @@ def _fail(what):
 def _format(format):
     f = _FORMATS.get(format)
     return f if f is not None else _fail(f"mx: format {format!r} is not one of {sorted(_FORMATS)}")
+
+
+def _no_gradient(t, what):
+    """Refuses a tensor that a gradient is to pass through, in either mode."""
+    if t.requires_grad and torch.is_grad_enabled():
+        _fail(f"{what}: no gradient passes through this call; detach it or use torch.no_grad()")
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        _fail(f"{what}: no gradient passes through this call; unpack the dual tensor")
 
 
 # the handle of a device's current stream; the public way to it builds a Stream object, which
@@ -151,8 +161,7 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
     f, type, shape = _format(format), _VALUES.get(x.dtype), tuple(x.shape)
     if type is None or not x.is_cuda or not shape or shape[-1] == 0:
         _fail("mx.quantize: a CUDA tensor (..., K) of BF16, FP16 or FP32")
-    if x.requires_grad and torch.is_grad_enabled():
-        _fail("mx.quantize: no gradient passes through it; detach x or use torch.no_grad()")
+    _no_gradient(x, "mx.quantize: x")
     if type != Z.VALUE_BF16 and x.is_neg():
         x = x.resolve_neg()  # a part of a conjugated complex tensor (of which BF16 has none)
     dev, cols = x.device, shape[-1]
@@ -173,6 +182,8 @@ def quantize(x, format="mxfp4", global_scale=None, stream=None):
             global_scale = torch.empty(1, dtype=torch.float32, device=dev)
         elif global_scale.dtype != torch.float32 or global_scale.numel() != 1 or global_scale.device != dev:
             _fail("mx.quantize: global_scale is one FP32 value on x's device")
+        else:
+            _no_gradient(global_scale, "mx.quantize: global_scale")
     elif global_scale is not None:
         _fail("mx.quantize: mxfp4 has no global_scale")
     if rows > 1 << 31 or cols > 1 << 30:
@@ -197,6 +208,7 @@ def _out(out, shape, dtype, device, what):
         _fail(f"{what}: out is a {dtype} tensor {tuple(shape)} on {device}")
     if out.is_neg():
         _fail(f"{what}: out is a negated view")
+    _no_gradient(out, f"{what}: out")
     if not (out.is_contiguous() or (out.dim() == 2 and (out.shape[1] == 1 or out.stride(1) == 1) and out.stride(0) >= out.shape[1])):
         _fail(f"{what}: out's rows are contiguous and do not overlap")
     return out

@@ -79,3 +79,33 @@ def test_a_pending_negation_is_taken(mx, Z):
     q = mx.quantize(x)
     with pytest.raises(Z.ZipnnError):
         mx.dequantize(q, torch.float32, out=z.conj().imag)
+
+
+def test_a_forward_gradient_is_refused(mx, Z):
+    import torch.autograd.forward_ad as fw
+    x = torch.ones(4, 64, device="cuda")
+    b = mx.quantize(torch.ones(8, 64, device="cuda"))
+    g = torch.ones(1, device="cuda")
+    with fw.dual_level():
+        d = fw.make_dual(x, torch.ones_like(x))
+        for call in (lambda: mx.quantize(d), lambda: mx.matmul(d, b), lambda: mx.dequantize(mx.quantize(x), torch.float32, out=d),
+                     lambda: mx.quantize(x, "nvfp4", fw.make_dual(g, torch.ones_like(g)))):
+            with pytest.raises(Z.ZipnnError):
+                call()
+        mx.matmul(x, b)  # a plain tensor beside it
+        mx.quantize(fw.unpack_dual(d).primal)
+
+
+def test_gradients_of_scales_and_outputs_are_refused(mx, Z):
+    x = torch.ones(4, 64, device="cuda")
+    q, g = mx.quantize(x), torch.ones(1, device="cuda", requires_grad=True)
+    out, prod = torch.zeros(4, 64, device="cuda", requires_grad=True), torch.zeros(4, 4, device="cuda", requires_grad=True)
+    calls = (lambda: mx.quantize(x, "nvfp4", g), lambda: mx.dequantize(q, torch.float32, out=out),
+             lambda: mx.matmul(q, q, torch.float32, out=prod))
+    for call in calls:
+        with pytest.raises(Z.ZipnnError):
+            call()
+    with torch.no_grad():
+        for call in calls:
+            call()
+    assert torch.equal(out.detach(), torch.ones(4, 64, device="cuda")) and (prod.detach() == 64).all()
