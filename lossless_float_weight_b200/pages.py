@@ -14,6 +14,7 @@ sequence holds which page (the references, lengths and tables of include/zipnn.h
 
 `fork`, `free`, `compact`, `copy` and `gather` only launch kernels on the current stream (or
 `stream`); what they find wrong is read with `status()`. `store` and `load` synchronise.
+No gradient passes through any of them, and pages that ask for one are refused.
 """
 import ctypes
 import math
@@ -21,7 +22,7 @@ import math
 import torch
 
 from . import zipnn as Z
-from .mx import _call, _fail, _use
+from .mx import _call, _fail, _no_gradient, _use
 
 
 def _codec_dtype(dtype, what):
@@ -74,6 +75,8 @@ def copy(src, src_ids, dst, dst_ids, count=None, ws=None, stream=None):
     if stream is not None:
         with _use(stream, dst.device):
             return copy(src, src_ids, dst, dst_ids, count, ws)
+    _no_gradient(src, "pages.copy: src")
+    _no_gradient(dst, "pages.copy: dst")
     a, na = _pool_desc(src, "pages.copy: src")
     b, nb = _pool_desc(dst, "pages.copy: dst")
     if na != nb or src.device != dst.device or a.planes != b.planes:
@@ -151,6 +154,7 @@ class PagePool:
         if stream is not None:
             with _use(stream, self.device):
                 return self.fork(rows, parents, lens)
+        _no_gradient(self.pages, "PagePool.fork: pages")
         rows, parents, lens = (_ids(v, self.device, "PagePool.fork") for v in (rows, parents, lens))
         n = rows.numel()
         if parents.numel() != n or lens.numel() != n or n > self._table.seqs:
@@ -164,6 +168,7 @@ class PagePool:
         if stream is not None:
             with _use(stream, self.device):
                 return self.free(rows, compact)
+        _no_gradient(self.pages, "PagePool.free: pages")
         rows = None if isinstance(rows, (tuple, list)) and not rows else _ids(rows, self.device, "PagePool.free")
         _call(Z.zipnn_pages_free, "zipnn_pages_free", self.device, self._pool_ref, self.page_bytes, self._table_ref,
               None if rows is None else rows.data_ptr(), 0 if rows is None else rows.numel(), compact, self._ws_ptr,

@@ -112,3 +112,22 @@ def test_lists_of_no_pages(P, Z):
     for bad in (lambda: P.copy(none[..., :32], None, pool.pages, None), lambda: pool.scatter(none[:1], [])):
         with pytest.raises(Z.ZipnnError):
             bad()
+
+
+def test_pages_that_ask_for_gradients_are_refused(P, Z):
+    import torch.autograd.forward_ad as fw
+    kv = torch.zeros(2, 8, 16, 8, device="cuda")
+    leaf = kv.clone().requires_grad_()
+    pool = P.PagePool(leaf, 16, 4, 4)
+    calls = (lambda: P.copy(leaf, [0], kv, [1]), lambda: P.copy(kv, [0], leaf, [1]), lambda: pool.fork([0], [-1], [20]),
+             lambda: pool.free([0], compact=True), lambda: pool.gather([0]))
+    for call in calls:
+        with pytest.raises(Z.ZipnnError):
+            call()
+    with torch.no_grad():
+        for call in calls:
+            call()
+    assert pool.status() == Z.OK
+    with fw.dual_level():
+        with pytest.raises(Z.ZipnnError):
+            P.copy(fw.make_dual(kv, torch.ones_like(kv)), [0], kv.clone(), [1])
