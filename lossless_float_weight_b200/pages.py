@@ -22,7 +22,7 @@ import math
 import torch
 
 from . import zipnn as Z
-from .mx import _call, _fail, _no_gradient, _use
+from .mx import _call, _fail, _no_gradient, _use, _written
 
 
 def _codec_dtype(dtype, what):
@@ -102,6 +102,7 @@ def copy(src, src_ids, dst, dst_ids, count=None, ws=None, stream=None):
     _call(Z.zipnn_pages_copy, "zipnn_pages_copy", dst.device, ctypes.byref(a),
           None if src_ids is None else src_ids.data_ptr(), ctypes.byref(b),
           None if dst_ids is None else dst_ids.data_ptr(), n, na, ws.data_ptr(), ws.numel())
+    _written((dst,))
     if wait:
         with torch.cuda.device(dst.device):
             Z.check(Z.status(ws), "pages.copy")
@@ -139,6 +140,7 @@ class PagePool:
                 slots < 1 or meta.numel() != P + max_seqs * (1 + slots) or (max_pages is not None and max_pages != slots):
             _fail("PagePool: meta is int32, pages + max_seqs x (1 + max_pages) long, beside the pages")
         self.pages, self.meta, self.page_tokens, self.device = pages, meta, page_tokens, pages.device
+        self._books = (pages, meta)  # what fork and compact write
         self.refs, self.lens = meta[:P], meta[P:P + max_seqs]
         self.tables = meta[P + max_seqs:].view(max_seqs, slots)
         self._table = Z.PageTableDesc(self.refs.data_ptr(), self.lens.data_ptr(), self.tables.data_ptr(), max_seqs, slots,
@@ -161,6 +163,7 @@ class PagePool:
             _fail("PagePool.fork: a parent and a length for each row, each row at most once")
         _call(Z.zipnn_pages_fork, "zipnn_pages_fork", self.device, self._pool_ref, self.page_bytes, self._table_ref, rows.data_ptr(),
               parents.data_ptr(), lens.data_ptr(), n, self._ws_ptr, self._ws_bytes)
+        _written(self._books)
 
     def free(self, rows, compact=False, stream=None):
         """The sequences in `rows` give their pages back; with compact, the gaps are closed
@@ -173,6 +176,7 @@ class PagePool:
         _call(Z.zipnn_pages_free, "zipnn_pages_free", self.device, self._pool_ref, self.page_bytes, self._table_ref,
               None if rows is None else rows.data_ptr(), 0 if rows is None else rows.numel(), compact, self._ws_ptr,
               self._ws_bytes)
+        _written(self._books if compact else (self.meta,))
 
     def compact(self, stream=None):
         """Close the gaps: afterwards the pages in use are the first `live` ones."""

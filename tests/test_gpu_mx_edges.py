@@ -109,3 +109,14 @@ def test_gradients_of_scales_and_outputs_are_refused(mx, Z):
         for call in calls:
             call()
     assert torch.equal(out.detach(), torch.ones(4, 64, device="cuda")) and (prod.detach() == 64).all()
+
+
+def test_an_output_saved_for_backward_is_seen_to_change(mx):
+    q = mx.quantize(torch.ones(4, 64, device="cuda"))
+    for write in (lambda o: mx.dequantize(q, torch.float32, out=o), lambda o: mx.matmul(q, mx.quantize(torch.ones(64, 64, device="cuda")), torch.float32, out=o)):
+        out = torch.zeros(4, 64, device="cuda")
+        w = torch.ones(4, 64, device="cuda", requires_grad=True)
+        y = (w * out).sum()  # out is saved
+        write(out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()

@@ -1,4 +1,5 @@
-"""Pages of a K/V cache: stores of rows that are damaged, loads that fail, lists of no pages."""
+"""Pages of a K/V cache: stores of rows that are damaged, loads that fail, lists of no pages, and
+what autograd is told of pages that change."""
 import pytest
 import torch
 
@@ -131,3 +132,39 @@ def test_pages_that_ask_for_gradients_are_refused(P, Z):
     with fw.dual_level():
         with pytest.raises(Z.ZipnnError):
             P.copy(fw.make_dual(kv, torch.ones_like(kv)), [0], kv.clone(), [1])
+
+
+def test_pages_saved_for_backward_are_seen_to_change(P):
+    def fork(pool):
+        pool.fork([1], [0], [20])
+
+    def scatter(pool):
+        pool.scatter(torch.zeros(2, 1, 16, 2, 64, dtype=torch.bfloat16, device="cuda"), [3])
+
+    def compact(pool):
+        pool.free([], compact=True)
+
+    def copy(pool):
+        P.copy(pool.pages, [0], pool.pages, [5])
+
+    for change in (fork, scatter, compact, copy):
+        pool = cache(P)
+        pool.fork([0], [-1], [40])
+        w = torch.ones_like(pool.pages, requires_grad=True)
+        y = (w * pool.pages).sum()  # the pages are saved
+        change(pool)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    pool = cache(P)
+    pool.fork([0], [-1], [40])
+    w = torch.ones_like(pool.pages, requires_grad=True)
+    y = (w * pool.pages).sum()
+    pool.free([0])  # changes no page
+    y.backward()
+    assert torch.equal(w.grad, pool.pages)
+    pool.fork([0], [-1], [40])
+    w = torch.ones(20, requires_grad=True, device="cuda")
+    y = w[pool.refs].sum()  # the references are saved as indexes
+    pool.free([0])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
