@@ -71,7 +71,13 @@ def _call(fn, what, device, *args):
 def _use(stream, device):
     """`stream` (a torch stream or a raw handle on `device`) as the current one: what a call
     allocates then belongs to the stream that writes it."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+    if device.type != "cuda":
+        _fail(f"a call on a stream: tensors on {device}")
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    elif stream.device != device:  # else the work would go to the current stream of the tensors' device
+        _fail(f"a stream of {stream.device} for tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _row_bytes(cols):
@@ -221,6 +227,8 @@ def _out(out, shape, dtype, device, what):
 
 def dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
     """The values of q as a tensor of its shape (BF16, FP16 or FP32)."""
+    if not isinstance(q, MxTensor):
+        _fail("mx.dequantize: an MxTensor")
     if stream is not None:
         with _use(stream, q.device):
             return dequantize(q, dtype, out)
