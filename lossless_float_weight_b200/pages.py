@@ -96,6 +96,8 @@ def copy(src, src_ids, dst, dst_ids, count=None, ws=None, stream=None):
         n = count
     if n == 0 or na == 0 or a.planes == 0:
         return dst
+    if ws is not None and ws.device != dst.device:
+        _fail("pages.copy: a workspace on the pages' device")
     wait = ws is None
     if wait:
         ws = copy_workspace(dst.device)

@@ -168,3 +168,12 @@ def test_pages_saved_for_backward_are_seen_to_change(P):
     pool.free([0])
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_a_workspace_elsewhere_is_refused(P, Z):
+    src, dst = torch.ones(2, 4, 16, 8, device="cuda"), torch.zeros(2, 4, 16, 8, device="cuda")
+    for ws in (torch.zeros(256, dtype=torch.uint8), torch.zeros(255, dtype=torch.uint8, device="cuda"),
+               torch.zeros(264, dtype=torch.uint8, device="cuda")[8:], torch.zeros(256, dtype=torch.uint8, device="meta")):
+        with pytest.raises(Z.ZipnnError):
+            P.copy(src, [0], dst, [1], ws=ws)
+    assert not dst.any()
