@@ -130,8 +130,8 @@ class PagePool:
     def __init__(self, pages, page_tokens, max_seqs, max_pages=None, meta=None):
         self._pool, self.page_bytes = _pool_desc(pages, "PagePool: pages")
         P = pages.shape[1]
-        if not 1 <= max_seqs <= 1 << 18 or page_tokens < 1:
-            _fail("PagePool: 1 to 2^18 sequences, page_tokens at least 1")
+        if not 1 <= max_seqs <= 1 << 18 or not 1 <= page_tokens < 1 << 31:
+            _fail("PagePool: 1 to 2^18 sequences, 1 to 2^31 - 1 positions of a page")
         if meta is None:
             if max_pages is None or max_pages < 1 or max_seqs * max_pages >= 1 << 31:
                 _fail("PagePool: max_pages, at least 1 (max_seqs x max_pages below 2^31), or meta")

@@ -177,3 +177,12 @@ def test_a_workspace_elsewhere_is_refused(P, Z):
         with pytest.raises(Z.ZipnnError):
             P.copy(src, [0], dst, [1], ws=ws)
     assert not dst.any()
+
+
+@pytest.mark.parametrize("tokens", [-1, 1 << 31, (1 << 32) + 16])
+def test_page_tokens_out_of_range_are_refused(P, Z, tokens):
+    with pytest.raises(Z.ZipnnError):
+        P.PagePool(torch.zeros(2, 4, 16, 8, device="cuda"), tokens, 4, 4)
+    pool = P.PagePool(torch.zeros(2, 4, 16, 8, device="cuda"), (1 << 31) - 1, 4, 4)
+    pool.fork([0], [-1], [(1 << 31) - 1])
+    assert pool.status() == Z.OK and pool.tables[0].tolist() == [0, -1, -1, -1]
