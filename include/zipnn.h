@@ -354,8 +354,9 @@ zipnn_status zipnn_mx_dequantize(zipnn_mx_format format, zipnn_value_type type, 
  * n. Products and scales are exact, sums are FP32 (the tensor cores' own), for NVFP4 times
  * the product of *a_global and *b_global, then rounded once to `type`. The order of a sum depends on the
  * sizes alone, so equal calls give equal bits. A NaN scale makes its row's results NaN.
- * At most 2^31 - 1 tiles of 128 x 128. Asynchronous, no workspace; a device-side wait that
- * gives up (never expected) leaves its part of `out` unwritten and sets the device's status. */
+ * At most 2^31 - 1 tiles of 128 x 128. Asynchronous, no workspace. A device-side wait that
+ * gives up (never expected) sets the device's status, and parts of `out` are then left as they
+ * were; what is written is right. */
 zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const void* a_scales, const float* a_global,
                              const void* b_codes, const void* b_scales, const float* b_global, uint64_t m, uint64_t n,
                              uint64_t k, zipnn_value_type type, void* out, uint64_t row_stride, zipnn_stream_t stream);
@@ -363,6 +364,13 @@ zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const 
 /* Wait for `stream`, then return and clear what zipnn_mx_matmul calls on the current device
  * set since this was last asked: ZIPNN_OK or ZIPNN_ERR_TIMEOUT. */
 zipnn_status zipnn_mx_status(zipnn_stream_t stream);
+
+/* Test aid (not a step of the product): waits of zipnn_mx_matmul's kernels give up after `polls`
+ * polls (0: at once; at most the default, 2^22) in the blocks whose number, masked with
+ * `mask`, is `value` (both at most 7; 0, 0: in all). (2^22, 0, 0) restores the default. It applies
+ * to calls made after it, in every host thread. A block that gives up stores nothing more, and
+ * ends when the copies and instructions that it has in flight have. */
+zipnn_status zipnn_test_mx_wait_limit(uint32_t polls, uint32_t mask, uint32_t value);
 
 /* ---- Pages of a K/V cache ------------------------------------------------------------
  * A served K/V cache lies in pages: page p of a pool holds `page_tokens` positions of one

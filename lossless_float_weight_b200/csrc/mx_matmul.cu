@@ -30,7 +30,13 @@ namespace {
 constexpr int kThreads = 192;
 constexpr uint32_t kStageBytesK = 128;  // code bytes of a row in a stage: 256 values
 constexpr uint32_t kStageK = 256, kMmaK = 64;
+// Polls after which a wait gives up (zipnn_test_mx_wait_limit lowers it for some blocks), and
+// always those of the waits that follow one that gave up: for what is still in flight. A poll
+// that finds nothing takes some microseconds.
 constexpr uint32_t kWaitPolls = 1u << 22;
+constexpr uint32_t kOtherPolls = 1u << 10;  // of the other blocks, while a limit is set for some
+constexpr uint32_t kNoLimit = kWaitPolls << 6;
+std::atomic<uint32_t> g_wait_limit{kNoLimit};  // polls << 6 | mask << 3 | value
 
 // ZIPNN_ERR_TIMEOUT after a wait that gave up, until zipnn_mx_status takes it.
 __device__ uint32_t g_mx_status;
@@ -44,7 +50,10 @@ struct Args {
   uint32_t col_tiles;          // scale tiles along a row
   uint32_t stages, mmas;       // of the whole row
   uint32_t split;              // blocks of a cluster, each a range of the stages
-  uint32_t depth, tmem_cols;
+  // One word: with eight bytes more of arguments a product takes 0.1 to 0.4 us longer.
+  // Blocks whose number, masked, is `value` (all of them, by default) wait for `polls`.
+  uint32_t depth : 3, value : 3, mask : 3, polls : 23;
+  uint32_t tmem_cols;
   int type, p_is_n;
 };
 
@@ -172,6 +181,19 @@ __device__ __forceinline__ float4 load_peer(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t load_peer_word(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t polls_of(const Args& a) { return (blockIdx.x & a.mask) == a.value ? a.polls : kOtherPolls; }
+// A whole warp's wait, of whose outcome its lanes agree, since they go on together. (A look at
+// `failed` in it, to give up where another wait has, costs a large product 5 to 17%.)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t polls) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, polls));
+}
+
 template <typename T>
 __device__ __forceinline__ T to_value(float v) {
   if constexpr (sizeof(T) == 4) return v;
@@ -226,10 +248,14 @@ __device__ __forceinline__ void store(const Args& a, uint32_t p, uint32_t q, flo
   else put<__half, N>(reinterpret_cast<__half*>(a.out) + at, step, a.q_rows - q, v);
 }
 
+// What a block of a cluster that gave up leaves in place of its sums: a NaN that no sum is, since
+// the tensor cores' is 0x7FFFFFFF.
+constexpr uint32_t kLost = 0x7FC0DEADu;
+
 // The sums of a block of a cluster lie in its shared memory as (columns / 4, 128 rows, 4).
 // This block's share of the columns of this thread's row: every SPLIT-th four, added over the
 // blocks in their order. Eight loads are in flight at a time (each takes a good part of a
-// microsecond).
+// microsecond). Nothing is stored where a block's sums are not whole (kLost).
 template <int FMT, int SPLIT>
 __device__ __forceinline__ void add_peers(const Args& a, const float4* sums, uint32_t rank, uint32_t used, uint32_t p, uint32_t q,
                                           const Scale& g) {
@@ -245,11 +271,22 @@ __device__ __forceinline__ void add_peers(const Args& a, const float4* sums, uin
     for (uint32_t k = 0; k < kAtOnce; k++) {
       if (c + k * SPLIT * 4 >= used) break;
       float4 v = t[k][0];
+      bool lost = false;
+#pragma unroll
+      for (int r = 0; r < SPLIT; r++) lost |= __float_as_uint(t[k][r].x) == kLost;
+      if (lost) return;
 #pragma unroll
       for (int r = 1; r < SPLIT; r++) v.x += t[k][r].x, v.y += t[k][r].y, v.z += t[k][r].z, v.w += t[k][r].w;
       store<FMT, 4>(a, p, q + c + k * SPLIT * 4, &v.x, g);
     }
   }
+}
+
+// Waits for the stages that were brought and not used and for the instructions issued, before the
+// block's memory goes to another one. Out of line, since it costs products up to 0.1 us in line.
+__device__ __noinline__ void drain(uint64_t* full, uint64_t* done, uint32_t issued, uint32_t brought, uint32_t depth) {
+  for (uint32_t i = issued; i < brought; i++) mbar_wait_bounded(full + i % depth, i / depth & 1, kWaitPolls);
+  mbar_wait_bounded(done, 0, kWaitPolls);
 }
 
 template <int FMT, int BN>
@@ -261,10 +298,10 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.depth * S::kStage);
   uint64_t *empty = full + a.depth, *done = empty + a.depth;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(done + 1);
-  volatile uint32_t* failed = tmem_at + 1;
+  volatile uint32_t *failed = tmem_at + 1, *brought = failed + 1, *issued = failed + 2;  // stages brought and used
 
   const uint32_t warp = uniform(threadIdx.x / 32);
-  const uint32_t tile = blockIdx.x / a.split, rank = blockIdx.x % a.split;
+  const uint32_t tile = blockIdx.x / a.split, rank = blockIdx.x % a.split, polls = polls_of(a);
   const uint32_t p0 = tile / a.q_tiles * 128, q0 = tile % a.q_tiles * BN;
   const uint32_t lo = (uint32_t)((uint64_t)a.stages * rank / a.split), hi = (uint32_t)((uint64_t)a.stages * (rank + 1) / a.split);
 
@@ -308,20 +345,22 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
   if (warp == 4) {
     const bool one = elect();
     Ring r;
-    for (uint32_t i = lo + early; i < hi; i++, r.next(a.depth)) {
-      if (!mbar_wait_bounded(empty + r.at, r.parity, kWaitPolls)) {
+    uint32_t i = lo + early;
+    for (; i < hi; i++, r.next(a.depth)) {
+      if (!warp_wait(empty + r.at, r.parity, polls)) {
         *failed = 1;
         break;
       }
       if (one) bring(i, r.at);
       __syncwarp();
     }
+    *brought = i - lo;
   } else if (warp == 5) {
     const bool one = elect();
     Ring r;
-    uint32_t left = a.mmas - lo * (kStageK / kMmaK);  // instructions to the end of the row
-    for (uint32_t i = lo; i < hi; i++, r.next(a.depth), left -= kStageK / kMmaK) {
-      if (!mbar_wait_bounded(full + r.at, r.parity, kWaitPolls)) {
+    uint32_t i = lo, left = a.mmas - lo * (kStageK / kMmaK);  // instructions to the end of the row
+    for (; i < hi; i++, r.next(a.depth), left -= kStageK / kMmaK) {
+      if (!warp_wait(full + r.at, r.parity, polls)) {
         *failed = 1;
         break;
       }
@@ -348,15 +387,20 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
     }
     if (one) commit(done);
     __syncwarp();
+    *issued = i - lo;
   } else {
-    if (!mbar_wait_bounded(done, 0, kWaitPolls)) *failed = 1;
+    if (!warp_wait(done, 0, polls)) *failed = 1;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   }
   __syncthreads();
-  if (*failed) {
-    if (threadIdx.x == 0) atomicMax(&g_mx_status, kStTimeout);
-  }
   const bool ok = *failed == 0;
+  if (!ok) {
+    if (threadIdx.x == 0) atomicMax(&g_mx_status, kStTimeout);
+    if (warp == 5) {
+      drain(full, done, *issued, *brought, a.depth);
+    }
+    __syncthreads();
+  }
   const Scale g = scale_of<FMT>(a);
   const uint32_t used = min((uint32_t)BN, a.q_rows - q0);  // columns that the output has
   if (a.split == 1) {
@@ -377,17 +421,22 @@ __global__ void __launch_bounds__(kThreads) k_mx_matmul(const __grid_constant__ 
       for (uint32_t c = 0; c < used; c += 16) {
         float v[16];
         load_sums(tmem + (warp * 32 << 16) + c, v);
+        if (!ok) {
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) sums[(c + i) / 4 * 128 + threadIdx.x] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int k = 0; k < 16; k++) v[k] = __uint_as_float(kLost);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) sums[(c + k) / 4 * 128 + threadIdx.x] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
       }
     }
     cluster_sync();
-    if (warp < 4 && ok) {
+    if (warp < 4) {
       const uint32_t p = p0 + threadIdx.x;
       if (a.split == 2) add_peers<FMT, 2>(a, sums, rank, used, p, q0, g);
       else if (a.split == 4) add_peers<FMT, 4>(a, sums, rank, used, p, q0, g);
       else add_peers<FMT, 8>(a, sums, rank, used, p, q0, g);
     }
+    __syncwarp();
     cluster_sync();
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -459,6 +508,16 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
                "h"((uint16_t)3)
                : "memory");
 }
+// Arrives at this block's barrier then.
+__device__ __forceinline__ void pair_commit_here(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void store_peer_word(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -488,10 +547,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kDepth * S::kStage);
   uint64_t *empty = full + S::kDepth, *sums_full = empty + S::kDepth, *sums_empty = sums_full + 1;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sums_empty + 1);
-  volatile uint32_t* failed = tmem_at + 1;
+  uint64_t* drained = reinterpret_cast<uint64_t*>(tmem_at + 2);
+  // a wait gave up, in either block; stages brought by this block, and those whose places were
+  // waited for; stages and tiles whose instructions the first block issued
+  volatile uint32_t *failed = tmem_at + 1, *brought = tmem_at + 4, *waited = tmem_at + 5, *issued = tmem_at + 6, *summed = tmem_at + 7;
 
   const uint32_t warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32, rank = blockIdx.x & 1;
-  const uint32_t pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const uint32_t pairs = gridDim.x / 2, pair = blockIdx.x / 2, polls = polls_of(a);
   const uint32_t tiles = (a.p_rows + 255) / 256 * a.q_tiles;
 
   // Stage i of a tile into place `at` of the ring: this block's share, whose bytes count at the
@@ -517,7 +579,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
       }
       mbar_init(sums_full, 1);
       mbar_init(sums_empty, 16);  // eight warps of two blocks
-      *failed = 0;
+      mbar_init(drained, 1);
+      *failed = *issued = *summed = 0;
     }
     __syncwarp();
   }
@@ -531,39 +594,44 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = uniform(*reinterpret_cast<volatile uint32_t*>(tmem_at));
 
+  const auto give_up = [&]() {
+    *failed = 1;
+    store_peer_word(peer(smem_addr(const_cast<uint32_t*>(failed)), rank ^ 1), 1);
+  };
   if (warp == 8) {
     const bool one = elect();
     Ring r;
     uint32_t n = 0;  // stages brought so far
-    for (uint32_t t = pair; t < tiles && !*failed; t += pairs) {
+    bool ok = true;
+    for (uint32_t t = pair; ok && t < tiles; t += pairs) {
       for (uint32_t i = 0; i < a.stages; i++, n++, r.next(S::kDepth)) {
-        if (n >= S::kDepth && !mbar_wait_bounded(empty + r.at, r.parity ^ 1, kWaitPolls)) {
-          *failed = 1;
-          break;
-        }
+        ok = n < S::kDepth || warp_wait(empty + r.at, r.parity ^ 1, polls);
+        if (!ok) break;
         if (one) bring(t, i, r.at);
         __syncwarp();
       }
     }
+    *brought = n;
     // the last arrivals at this block's barriers, which the other block's thread sends
-    for (uint32_t k = 0; k < S::kDepth && !*failed; k++, n++, r.next(S::kDepth))
-      if (n >= S::kDepth && !mbar_wait_bounded(empty + r.at, r.parity ^ 1, kWaitPolls)) *failed = 1;
+    for (uint32_t k = 0; ok && k < S::kDepth; k++) {
+      ok = n < S::kDepth || warp_wait(empty + r.at, r.parity ^ 1, polls);
+      if (ok) n++, r.next(S::kDepth);
+    }
+    *waited = n;
+    if (!ok) give_up();
   } else if (warp == 9 && rank == 0) {
     const bool one = elect();
     Ring r;
-    uint32_t turn = 0;  // parity of the tiles that the sums have left
-    for (uint32_t t = pair; t < tiles && !*failed; t += pairs, turn ^= 1) {
-      if (t != pair && !mbar_wait_bounded(sums_empty, turn ^ 1, kWaitPolls)) {
-        *failed = 1;
-        break;
-      }
+    bool ok = true;
+    uint32_t n = 0, turns = 0;  // stages and tiles whose instructions were issued
+    for (uint32_t t = pair; t < tiles; t += pairs, turns++) {
+      ok = t == pair || warp_wait(sums_empty, (turns & 1) ^ 1, polls);
+      if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       uint32_t left = a.mmas;
-      for (uint32_t i = 0; i < a.stages; i++, r.next(S::kDepth), left -= kStageK / kMmaK) {
-        if (!mbar_wait_bounded(full + r.at, r.parity, kWaitPolls)) {
-          *failed = 1;
-          break;
-        }
+      for (uint32_t i = 0; i < a.stages; i++, n++, r.next(S::kDepth), left -= kStageK / kMmaK) {
+        ok = warp_wait(full + r.at, r.parity, polls);
+        if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t st = smem_addr(smem) + r.at * S::kStage, sc = st + S::kP + S::kQ;
         const uint32_t tp = tmem + BN + r.at * S::kScaleCols, tq = tp + 4 * S::kTiles;
@@ -587,9 +655,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
         }
         __syncwarp();
       }
+      if (!ok) break;  // no block hears of sums that are not whole
       if (one) pair_commit(sums_full);
       __syncwarp();
     }
+    *issued = n, *summed = turns;
+    if (!ok) give_up();
   } else if (warp < 8) {
     const Scale g = scale_of<FMT>(a);
     const uint32_t quarter = warp % 4, half = warp / 4, leader_bar = peer(smem_addr(sums_empty), 0);
@@ -597,8 +668,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
     uint32_t k_tile = 0;
     for (uint32_t t = pair; t < tiles; t += pairs, k_tile++) {
       const uint32_t p = t / a.q_tiles * 256 + rank * 128 + quarter * 32 + lane, q = t % a.q_tiles * BN + half * kCols;
-      if (!mbar_wait_bounded(sums_full, k_tile & 1, kWaitPolls)) {
-        *failed = 1;
+      if (!warp_wait(sums_full, k_tile & 1, polls)) {
+        give_up();
         break;
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -609,7 +680,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive_at(leader_bar);
-      if (!*failed) store<FMT, kCols>(a, p, q, v, g);
+      store<FMT, kCols>(a, p, q, v, g);
     }
     __syncwarp();
   }
@@ -617,7 +688,40 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_matmul_pair(const __grid
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   cluster_sync();  // neither block's barriers and tensor memory go while the other still uses them
-  if (*failed && threadIdx.x == 0) atomicMax(&g_mx_status, kStTimeout);
+  if (*failed) {  // the same in both blocks by now
+    if (threadIdx.x == 0) atomicMax(&g_mx_status, kStTimeout);
+    if (warp == 8 || warp == 0) {
+      // the arrivals that are still to come for instructions issued: one a stage at `empty`, one
+      // a tile at sums_full
+      const uint32_t stages = load_peer_word(peer(smem_addr(const_cast<uint32_t*>(issued)), 0));
+      const uint32_t sums = load_peer_word(peer(smem_addr(const_cast<uint32_t*>(summed)), 0));
+      if (warp == 0) {
+        if (sums) mbar_wait_bounded(sums_full, (sums - 1) & 1, kWaitPolls);
+      } else {
+        // the first kDepth places held no stage yet
+        for (uint32_t s = *waited < S::kDepth ? 0 : *waited - S::kDepth; s < stages; s++)
+          mbar_wait_bounded(empty + s % S::kDepth, s / S::kDepth & 1, kWaitPolls);
+      }
+    } else if (warp == 9 && rank == 0) {
+      if (elect()) pair_commit_here(drained);
+      __syncwarp();
+      mbar_wait_bounded(drained, 0, kWaitPolls);
+      // the stages brought and not used, at most one in each place. Where only one block has
+      // brought its half, the other's bytes, which will not come, are taken off the count.
+      const uint32_t first = *brought, second = load_peer_word(peer(smem_addr(const_cast<uint32_t*>(brought)), 1));
+      for (uint32_t s = *issued; s < max(first, second); s++) {
+        uint64_t* bar = full + s % S::kDepth;
+        if (elect()) {
+          if (s >= first) mbar_expect_tx(bar, S::kBytes);
+          else if (s >= second) complete_tx(bar, S::kBytes);
+        }
+        __syncwarp();
+        mbar_wait_bounded(bar, s / S::kDepth & 1, kWaitPolls);
+      }
+    }
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == 9) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
@@ -802,9 +906,17 @@ zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const 
   g.mmas = (uint32_t)mx_div_up(k, kMmaK);
   g.type = type;
   g.p_is_n = p_is_n;
+  const uint32_t limit = g_wait_limit.load(std::memory_order_relaxed);
+  g.polls = limit >> 6, g.mask = limit >> 3 & 7, g.value = limit & 7;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = format == ZIPNN_MXFP4 ? launch_matmul<kMxFp4>(pairs, p, q, k, g, st) : launch_matmul<kNvFp4>(pairs, p, q, k, g, st);
   return e == cudaSuccess ? ZIPNN_OK : ZIPNN_ERR_CUDA;
+}
+
+zipnn_status zipnn_test_mx_wait_limit(uint32_t polls, uint32_t mask, uint32_t value) {
+  if (mask > 7 || value > 7) return ZIPNN_ERR_INVALID_ARG;
+  g_wait_limit.store(std::min(polls, kWaitPolls) << 6 | mask << 3 | value, std::memory_order_relaxed);
+  return ZIPNN_OK;
 }
 
 zipnn_status zipnn_mx_status(zipnn_stream_t stream) {

@@ -94,6 +94,7 @@ zipnn_mx_dequantize = _sig("zipnn_mx_dequantize", _i, _i, _i, _vp, _vp, _vp, _u6
 
 zipnn_mx_matmul = _sig("zipnn_mx_matmul", _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _u64, _u64, _u64, _i, _vp, _u64, _vp)
 zipnn_mx_status = _sig("zipnn_mx_status", _i, _vp)
+zipnn_test_mx_wait_limit = _sig("zipnn_test_mx_wait_limit", _i, _u32, _u32, _u32)
 
 
 class PagePoolDesc(ctypes.Structure):
@@ -120,7 +121,7 @@ C_ABI_NAMES = [
     "zipnn_kernel_name", "zipnn_compress_noalloc", "zipnn_decompress_batch_workspace_bytes",
     "zipnn_decompress_batch", "zipnn_test_lookback_limit", "zipnn_shard_workspace_bytes", "zipnn_shard_sizes",
     "zipnn_shard_tables", "zipnn_mx_row_bytes", "zipnn_mx_scale_bytes", "zipnn_mx_quantize", "zipnn_mx_dequantize",
-    "zipnn_mx_matmul", "zipnn_mx_status", "zipnn_pages_workspace_bytes", "zipnn_pages_copy", "zipnn_pages_fork", "zipnn_pages_free",
+    "zipnn_mx_matmul", "zipnn_mx_status", "zipnn_test_mx_wait_limit", "zipnn_pages_workspace_bytes", "zipnn_pages_copy", "zipnn_pages_fork", "zipnn_pages_free",
 ]
 
 

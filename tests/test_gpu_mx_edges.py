@@ -120,3 +120,28 @@ def test_an_output_saved_for_backward_is_seen_to_change(mx):
         write(out)
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.backward()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_a_product_over_the_longest_rows(mx, Z, fmt):
+    """2^30 - 7 products to a sum, in 2^22 stages over a cluster: values in the first columns, in
+    those where the scale tiles pass 2^31 and 2^32 bytes, and in the last."""
+    cols = (1 << 30) - 7
+    f = {"mxfp4": Z.MXFP4, "nvfp4": Z.NVFP4}[fmt]
+    rng = np.random.RandomState(2)
+    at = np.unique(np.concatenate([np.arange(40), (1 << 28) + np.arange(-40, 40), (1 << 29) + np.arange(-40, 40), cols - 1 - np.arange(40)]))
+    ones = {"mxfp4": 127, "nvfp4": 0x38}[fmt]
+    parts = []
+    for rows in (2, 3):
+        v = rng.randint(1, 8, (rows, at.size))  # codes of positive values
+        codes = torch.zeros(rows, Z.zipnn_mx_row_bytes(cols), dtype=torch.uint8, device="cuda")
+        for odd in (0, 1):
+            i = torch.from_numpy(at[at % 2 == odd] // 2).cuda()
+            codes[:, i] |= torch.from_numpy(v[:, at % 2 == odd].astype(np.uint8) << (4 * odd)).cuda()
+        scales = torch.full((Z.zipnn_mx_scale_bytes(f, rows, cols),), ones, dtype=torch.uint8, device="cuda")
+        g = torch.ones(1, device="cuda") if fmt == "nvfp4" else None
+        parts.append((mx.MxTensor(codes, scales, (rows, cols), fmt, g), U.GRID[v]))
+    (a, va), (b, vb) = parts
+    y = mx.matmul(a, b, torch.float32)
+    assert mx.status() == Z.OK
+    assert np.array_equal(y.double().cpu().numpy(), va @ vb.T)

@@ -81,3 +81,9 @@ def test_tile_scales_is_the_documented_layout(Z):
         for b in range(9):
             want[512 * (r // 128 * 3 + b // 4) + 16 * (r % 32) + 4 * (r // 32 % 4) + b % 4] = s[r, b]
     assert torch.equal(t, want)
+
+
+def test_wait_limit_is_a_host_setting(Z):
+    assert Z.zipnn_test_mx_wait_limit(0, 7, 3) == Z.OK
+    assert Z.zipnn_test_mx_wait_limit(0, 8, 0) == Z.ERR_INVALID_ARG and Z.zipnn_test_mx_wait_limit(0, 0, 8) == Z.ERR_INVALID_ARG
+    assert Z.zipnn_test_mx_wait_limit(1 << 22, 0, 0) == Z.OK  # back to the default
