@@ -2,9 +2,10 @@
 //
 // Both are one pass over the data with a few operations a value, so HBM bounds them: BF16 to
 // MXFP4 moves 2 + 0.5 + 1/32 bytes a value each way. Measured on 11008 x 4096 BF16 (114 MB in
-// all): MXFP4 19 us (6.0 TB/s), NVFP4 with a given scale 25 us (its border tests: 13 M warp
-// instructions, MXFP4's 8 M), with its scale found 43 us (amax reads x once more, 17.5 us);
-// read back 20.5 us (5.6 TB/s).
+// all): MXFP4 19 us (6.0 TB/s), NVFP4 with a given scale 26 us (16.4 M warp instructions for
+// MXFP4's 8.2 M: half of the issue slots and 44% of the memory rate, with 42% of the warps, so
+// that neither is full: it waits for its loads), with its scale found 40 to 45 us (amax reads x
+// once more, 17.5 us); read back 20 us (5.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -225,7 +226,9 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
 }
 
 // What quotients are taken with, so that one is below the exact one and one above it: FP32
-// factors and products are off by less than 2^-22 here.
+// factors and products are off by at most 5 x 2^-24 here (nv_codes: s g, this factor and the last
+// product half a step each, the reciprocal a whole one; nv_scale: four half steps), which is
+// less than 2^-21.
 constexpr float kBelow = 1.f - 0x1p-21f, kAbove = 1.f + 0x1p-21f;
 
 // Where 1 / g and what is done with it below are ordinary numbers.
@@ -627,7 +630,7 @@ cudaError_t launch_quantize(const Matrix& m, float* global_scale, bool find, uin
 template <int FMT, int TYPE>
 cudaError_t launch_dequantize(const Packed& m, uint8_t* out, uint64_t stride_bytes, cudaStream_t st) {
   TimedLaunch t(kIdMxDequantize, st);
-  // 11008 x 4096 to BF16 takes 21.5 us by the one, 11008 x 4097 34 us by the other
+  // 11008 x 4096 to BF16 takes 20 us by the one, 11008 x 4097 30 us by the other
   if (reinterpret_cast<uintptr_t>(out) % 32 == 0 && stride_bytes % 32 == 0) {
     const Cover c = cover(m.rows, mx_div_up(m.cols, kReadBack), kReadGrid);
     k_mx_dequantize<FMT, TYPE><<<c.grid, kThreads, 0, st>>>(m, out, stride_bytes, c);

@@ -7,10 +7,11 @@
 // as tcgen05.cp takes them. One thread feeds TMA, one issues the matrix instructions (K = 64
 // each, accumulating FP32 in tensor memory), four warps read the sums back and store them.
 //
-// What bounds it: few rows, HBM behind 2.7 us of launch, first load and sums (1 x 11008 x 4096,
-// 24 MB: 7.1 us; 1 x 32000 x 4096, 70 MB: 13.9 us, 5.0 TB/s); many rows, the way from L2 to
-// shared memory and, repeated, the 1000 W limit (4096 x 11008 x 4096: 74 us, 5.0 PFLOP/s; back
-// to back 89 us at 1.6 GHz).
+// What bounds it: few rows, what the busy SMs can draw behind 2.7 us of launch, first load and
+// sums (1 x 11008 x 4096, 86 blocks and 24 MB: MXFP4 8.7 us and NVFP4 9.6 us where the weights come
+// from HBM, over 450 MB of them in turn, 6.9 and 8.1 us where they lie in L2); many rows, the way
+// from L2 to shared memory and, repeated, the 1000 W limit (4096 x 11008 x 4096: 72 us, 5.1 PFLOP/s,
+// and 77 us in NVFP4; back to back 88 us at 1.6 GHz).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -12,8 +12,11 @@ sequence holds which page (the references, lengths and tables of include/zipnn.h
     pool.free([0], compact=True)         # its references back, and the gaps closed
     pool.load(stored, 2)                 # the same positions in row 2
 
-`fork`, `free`, `compact`, `copy` and `gather` only launch kernels on the current stream (or
-`stream`); what they find wrong is read with `status()`. `store` and `load` synchronise.
+`fork`, `free`, `compact`, `copy`, `gather` and `scatter` launch kernels on the current stream (or
+`stream`), and do no more where their lists are int32 tensors on the device: a Python list is
+copied there first, which waits and cannot be captured. What they find wrong is read with
+`status()`. `copy` without a workspace, `store` and `load` synchronise. The calls on one pool
+share its books and its workspace: on several streams, the caller has them follow one another.
 No gradient passes through any of them, and pages that ask for one are refused.
 """
 import ctypes
@@ -34,7 +37,8 @@ def _codec_dtype(dtype, what):
 
 
 def copy_workspace(device="cuda"):
-    """A workspace for `copy`: its status stays at the first error until it is zeroed."""
+    """A workspace for `copy`, to be kept between calls (making one takes longer than a small
+    copy): its status stays at the first error until it is zeroed."""
     return torch.zeros(256, dtype=torch.uint8, device=device)
 
 
