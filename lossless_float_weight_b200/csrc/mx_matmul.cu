@@ -885,8 +885,11 @@ zipnn_status zipnn_mx_matmul(zipnn_mx_format format, const void* a_codes, const 
     return ZIPNN_ERR_INVALID_ARG;
   if (mx_div_up(m, 128) * mx_div_up(n, 128) > 0x7FFFFFFFull) return ZIPNN_ERR_INVALID_ARG;
   if (!device_ok()) return ZIPNN_ERR_UNSUPPORTED;
-  // Large products go to pairs of blocks (1024 x 4096 x 4096, 64 tiles: 11.6 us, 12.7 by single
-  // blocks; 512 x 4096 x 4096, 32 tiles: 10.8 and 9.0). B's rows lie along the 128 rows of a
+  // Large products go to pairs of blocks (MXFP4, by pairs and by single blocks: 1024 x 4096 x 4096,
+  // 64 tiles, 10.8 and 11.8 us; 640 x 4096 x 4096, 48 tiles, 10.4 and 11.0; 512 x 4096 x 4096, 32
+  // tiles, 10.4 and 8.5; 512 x 11008 x 4096, 86 tiles, 16.5 and 17.1). Padding is not looked at:
+  // 300 x 11008 x 4096, where nearly half of each tile is padding, takes 16.9 us, and would take
+  // 11.6. B's rows lie along the 128 rows of a
   // block, whose lanes then hold neighbours of the output (4096 x 256 x 4096: 9 us, 19 with A's),
   // unless they are few and A's are more.
   const bool pairs = m > 128 && n > 128 && mx_div_up(m, 256) * mx_div_up(n, 256) >= 40;
