@@ -58,6 +58,7 @@ struct Args {
   int type, p_is_n;
 };
 
+constexpr uint32_t kAllShared = 227 * 1024;  // of an SM
 constexpr uint32_t kSmallest = 80 * 1024;  // below the shared memory of every block here
 
 template <int FMT, int BN>
@@ -79,11 +80,11 @@ struct Shape {
     const uint32_t used = BN + depth * kScaleCols;
     return used <= 64 ? 64 : used <= 128 ? 128 : used <= 256 ? 256 : 512;
   }
-  static_assert(smem(kAlone) <= 227 * 1024 && BN + kAlone * kScaleCols <= 512, "one block to an SM");
+  static_assert(smem(kAlone) <= kAllShared && BN + kAlone * kScaleCols <= 512, "one block to an SM");
   // Two blocks on an SM, of one call or of two, never wait for each other's tensor memory
   // (which could close a ring of clusters): a block that leaves room for another one's shared
   // memory takes at most half of it.
-  static_assert(cols(kShared) <= 256 && (cols(kAlone) <= 256 || smem(kAlone) + kSmallest > 227 * 1024), "tensor memory");
+  static_assert(cols(kShared) <= 256 && (cols(kAlone) <= 256 || smem(kAlone) + kSmallest > kAllShared), "tensor memory");
 };
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -468,10 +469,9 @@ struct PairShape {
   static constexpr uint32_t kBytes = kP + kQ + kSp + kSq;
   static constexpr uint32_t kStage = (kBytes + 1023) / 1024 * 1024;
   static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kHalves);
-  static constexpr uint32_t kFit = (227 * 1024 - 1024 - 512) / kStage, kRoom = (512 - BN) / kScaleCols;
+  static constexpr uint32_t kFit = (kAllShared - 1024 - 512) / kStage, kRoom = (512 - BN) / kScaleCols;
   static constexpr uint32_t kDepth = kFit < kRoom ? kFit : kRoom;
-  static constexpr uint32_t kSmem = kDepth * kStage + 1024 + 512;
-  static_assert(kSmem + kSmallest > 227 * 1024, "all of the tensor memory, so no other block on the SM");
+  static_assert(kDepth * kStage + 1024 + 512 <= kAllShared, "one block to an SM, with all of the tensor memory");
 };
 
 __device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
@@ -777,7 +777,7 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, uint64_t cols, Args
   cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_mx_matmul<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem(S::kAlone));
+    e = cudaFuncSetAttribute(k_mx_matmul<FMT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAllShared);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -796,7 +796,10 @@ cudaError_t launch_tiles(const Operand& p, const Operand& q, uint64_t cols, Args
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((uint32_t)(tiles * a.split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::smem(a.depth);
+  // Blocks that wait for each other have their SMs to themselves: beside another library's, which
+  // may wait for its neighbours as well, two clusters could hold the tensor memory that the
+  // other needs. It takes no time, since each block has an SM anyway.
+  cfg.dynamicSmemBytes = a.split > 1 ? kAllShared : S::smem(a.depth);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -827,7 +830,7 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, uint64_t cols, Args
   cudaError_t e = device_sms(dev, sms);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_mx_matmul_pair<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    e = cudaFuncSetAttribute(k_mx_matmul_pair<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAllShared);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -842,7 +845,7 @@ cudaError_t launch_pairs(const Operand& p, const Operand& q, uint64_t cols, Args
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((uint32_t)(2 * (tiles < most ? tiles : most)));
   cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.dynamicSmemBytes = kAllShared;  // no other block beside these either
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
