@@ -273,10 +273,12 @@ __device__ __forceinline__ void add_peers(const Args& a, const float4* sums, uin
     for (uint32_t k = 0; k < kAtOnce; k++) {
       if (c + k * SPLIT * 4 >= used) break;
       float4 v = t[k][0];
-      bool lost = false;
+      if (k == 0 && c == rank * 4) {  // all of a block's sums are marked, or none
+        bool lost = false;
 #pragma unroll
-      for (int r = 0; r < SPLIT; r++) lost |= __float_as_uint(t[k][r].x) == kLost;
-      if (lost) return;
+        for (int r = 0; r < SPLIT; r++) lost |= __float_as_uint(t[k][r].x) == kLost;
+        if (lost) return;
+      }
 #pragma unroll
       for (int r = 1; r < SPLIT; r++) v.x += t[k][r].x, v.y += t[k][r].y, v.z += t[k][r].z, v.w += t[k][r].w;
       store<FMT, 4>(a, p, q + c + k * SPLIT * 4, &v.x, g);
