@@ -162,10 +162,10 @@ def tile_scales(block_scales):
 def quantize(x, format="mxfp4", global_scale=None, stream=None):
     """Quantise the CUDA tensor x (..., K) in blocks along its last dimension.
 
-    nvfp4: global_scale is a one-element FP32 CUDA tensor (positive; taken as it is, and kept by
-    the result, whose values change with it), or None: then it is found from x (its largest
-    finite magnitude / 2688). Rounding, saturation and
-    what a block with a NaN gives: zipnn_mx_quantize."""
+    nvfp4: global_scale is a one-element FP32 CUDA tensor (positive and finite; taken as it is,
+    and kept by the result, whose values change with it), or None: then it is found from x (its
+    largest finite magnitude / 2688). Rounding, saturation and what a block with a NaN gives:
+    zipnn_mx_quantize."""
     if stream is not None:
         with _use(stream, x.device):
             return quantize(x, format, global_scale)

@@ -189,7 +189,8 @@ class PagePool:
         self.free((), compact=True, stream=stream)
 
     def gather(self, ids, out=None, stream=None):
-        """The pages `ids` as a contiguous (planes, len(ids), ...) tensor."""
+        """The pages `ids` as a contiguous (planes, len(ids), ...) tensor. What a number outside
+        the pool (which the status tells of) or below 0 stands for is left as it was in `out`."""
         if stream is not None:
             with _use(stream, self.device):
                 return self.gather(ids, out)
@@ -253,10 +254,11 @@ class PagePool:
         shape = self.pages.shape[:1] + (-(-stored.length // self.page_tokens),) + self.pages.shape[2:]
         with torch.cuda.device(self.device):
             flat = Z.decompress(stored.container, codec, shape, stored.chunk_bytes).view(dt)
-        self.fork([row], [-1], [stored.length])
+        mine = _ids([row], self.device, "PagePool.load")  # at hand for the way back, which allocates nothing
+        self.fork(mine, [-1], [stored.length])
         Z.check(self.status(clear=True), "PagePool.load: no room")
         try:
             copy(flat, None, self.pages, self._held(row)[1])  # with a status of its own: waits, and raises
         except BaseException:  # whatever it was, the row is empty again
-            self.free([row])
+            self.free(mine)
             raise

@@ -87,6 +87,34 @@ def test_a_load_that_fails_leaves_the_books_as_they_were(P, Z, monkeypatch, wher
     assert pool.lens.tolist() == [0, 33, 70, 0, 0, 0]
 
 
+def test_a_load_that_fails_needs_no_memory_to_undo(P, Z, monkeypatch):
+    """As on a device that the cache fills: after the failure nothing can be allocated."""
+    pool = cache(P)
+    pool.fork([0, 1], [-1, -1], [70, 33])
+    stored = pool.store(0)
+    pool.free([0])
+    books = pool.meta.clone()
+    full = []
+
+    def no_memory(*a, **k):
+        full.append(1)
+        raise torch.cuda.OutOfMemoryError("out of memory")
+
+    ids = P._ids
+
+    def allocating(v, device, what):
+        if full and not isinstance(v, torch.Tensor):
+            raise torch.cuda.OutOfMemoryError("out of memory")
+        return ids(v, device, what)
+
+    with monkeypatch.context() as m:
+        m.setattr(P, "copy", no_memory)
+        m.setattr(P, "_ids", allocating)
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            pool.load(stored, 2)
+    assert torch.equal(pool.meta, books) and pool.status() == Z.OK
+
+
 def test_a_stored_sequence_on_another_device_is_refused(P, Z):
     pool = cache(P)
     pool.fork([0], [-1], [70])
